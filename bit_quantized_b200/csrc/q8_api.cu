@@ -92,6 +92,29 @@ q8_status launch_status(cudaError_t e) {
     return Q8_ERR_LAUNCH;
 }
 
+// Block-scaled FP8: rows and columns up to 65535 blocks of 128 (grid
+// dimensions of the quantizers).
+constexpr int64_t kMaxBlockDim = int64_t(65535) * 128;
+
+int64_t blocks128(int64_t v) { return (v + 127) / 128; }
+int64_t block_codes_bytes(int64_t m, int64_t k) { return (m * k + 255) / 256 * 256; }
+int64_t block_scale_bytes(int64_t m, int64_t k) { return (4 * m * blocks128(k) + 255) / 256 * 256; }
+
+q8_status check_weight_block(const q8_weight_block* w, int64_t experts) {
+    if (!w) return Q8_ERR_NULL;
+    if (experts < 1 || w->n < 0 || w->k <= 0 || w->n > kMaxDim || w->k > kMaxBlockDim || w->k % 32 != 0 ||
+        w->n % experts != 0 || (w->n / experts) % 16 != 0 || w->n / experts > kMaxBlockDim || w->ld < w->k)
+        return Q8_ERR_SHAPE;
+    if (w->n > 0 && (!w->codes || !w->scale)) return Q8_ERR_NULL;
+    if (!aligned16(w->codes) || !aligned16(w->scale) || w->ld % 16 != 0) return Q8_ERR_ALIGN;
+    return Q8_OK;
+}
+
+// Output tiles of a block-scaled linear are counted in 32 bits.
+bool block_tiles_fit(int64_t m, int64_t n, int64_t experts) {
+    return ((m + 255) / 256 + experts) * blocks128(n) <= kMaxDim;
+}
+
 q8_status check_weight(const q8_weight* w) {
     if (!w) return Q8_ERR_NULL;
     if (w->n < 0 || w->k <= 0 || w->n > kMaxDim || w->k > kMaxDim || w->k % 32 != 0 ||
@@ -161,7 +184,12 @@ q8_status q8_inject_failure(q8_status code, int32_t skip) {
 }
 
 size_t q8_workspace_size(int op, int64_t m, int64_t n, int64_t k) {
-    if (op != Q8_OP_LINEAR_INT8_MIXED || m < 0 || n < 0 || k < 0) return 0;
+    if (m < 0 || n < 0 || k < 0) return 0;
+    if (op == Q8_OP_LINEAR_FP8_BLOCK) {
+        if (m > kMaxBlockDim || n > kMaxBlockDim || k > kMaxBlockDim) return SIZE_MAX;
+        return m <= kBlockFusedTokens ? 0 : static_cast<size_t>(block_codes_bytes(m, k) + block_scale_bytes(m, k));
+    }
+    if (op != Q8_OP_LINEAR_INT8_MIXED) return 0;
     // Beyond 2^31 - 1 no call is valid; the products below would also be
     // able to overflow int64 there.
     if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return SIZE_MAX;
@@ -621,6 +649,134 @@ q8_status q8_linear_fp8_grouped(const q8_act* x, const q8_weight* w, int64_t num
     a.bias = bias;
     a.y = static_cast<__nv_bfloat16*>(Y); a.ldy = ldy;
     return launch_moe_fp8(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_quantize_act_block(const void* X, q8_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                void* codes, float* scale, q8_stream_t stream) {
+    if (m < 0 || k <= 0 || m > kMaxBlockDim || k > kMaxBlockDim || k % 32 != 0 || ldx < k) return Q8_ERR_SHAPE;
+    if (!float_input(x_dtype)) return Q8_ERR_DTYPE;
+    if (m == 0) return Q8_OK;   // empty call
+    if (!X || !codes || !scale) return Q8_ERR_NULL;
+    if (!aligned16(X) || !ld_ok(ldx, k, x_dtype) || !aligned16(codes) || !aligned16(scale)) return Q8_ERR_ALIGN;
+    q8_status st = check_device();
+    if (st != Q8_OK) return st;
+    BlockQuantArgs a = {};
+    a.src = X; a.src_dtype = x_dtype;
+    a.stack = 1; a.rows = m; a.k = k; a.ld = ldx;
+    a.codes = codes; a.scale = scale;
+    return launch_status(launch_block_quant(a, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+q8_status q8_quantize_weight_block(const void* W, q8_dtype w_dtype, int64_t experts, int64_t n, int64_t k,
+                                   int64_t ldw, void* codes, float* scale, q8_stream_t stream) {
+    if (experts < 0 || experts > 65535 || n < 0 || k <= 0 || n > kMaxBlockDim || k > kMaxBlockDim ||
+        experts * n > kMaxDim || k % 32 != 0 || n % 16 != 0 || ldw < k)
+        return Q8_ERR_SHAPE;
+    if (!float_input(w_dtype)) return Q8_ERR_DTYPE;
+    if (experts == 0 || n == 0) return Q8_OK;   // empty call
+    if (!W || !codes || !scale) return Q8_ERR_NULL;
+    if (!aligned16(W) || !ld_ok(ldw, k, w_dtype) || !aligned16(codes) || !aligned16(scale)) return Q8_ERR_ALIGN;
+    q8_status st = check_device();
+    if (st != Q8_OK) return st;
+    BlockQuantArgs a = {};
+    a.src = W; a.src_dtype = w_dtype;
+    a.stack = experts; a.rows = n; a.k = k; a.ld = ldw;
+    a.codes = codes; a.scale = scale;
+    return launch_status(launch_block_quant(a, true, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+q8_status q8_linear_fp8_block(const q8_act_block* x, const q8_weight_block* w, const float* bias, void* Y,
+                              int64_t ldy, q8_stream_t stream) {
+    if (!x || !w) return Q8_ERR_NULL;
+    q8_status st = check_weight_block(w, 1);
+    if (st != Q8_OK) return st;
+    if (x->m < 0 || x->m > kMaxBlockDim || x->k != w->k || x->ld < x->k || ldy < w->n ||
+        !block_tiles_fit(x->m, w->n, 0))
+        return Q8_ERR_SHAPE;
+    if (x->m == 0 || w->n == 0) return Q8_OK;   // empty call
+    if (!x->codes || !x->scale || !Y) return Q8_ERR_NULL;
+    if (!aligned16(x->codes) || x->ld % 16 != 0 || !aligned16(x->scale) || !aligned16(Y) || ldy % 8 != 0 ||
+        (bias && !aligned16(bias)))
+        return Q8_ERR_ALIGN;
+    st = check_device();
+    if (st != Q8_OK) return st;
+    BlockLinearArgs a = {};
+    a.m = x->m; a.n = w->n; a.k = w->k;
+    a.x_codes = x->codes; a.sx = x->scale; a.ldx = x->ld;
+    a.experts = 1;
+    a.w_codes = w->codes; a.ldw = w->ld; a.sw = w->scale;
+    a.bias = bias;
+    a.y = static_cast<__nv_bfloat16*>(Y); a.ldy = ldy;
+    return launch_block_linear(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_linear_fp8_block_dynamic(const void* X, q8_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                      const q8_weight_block* w, const float* bias, void* Y, int64_t ldy,
+                                      void* workspace, size_t ws_bytes, q8_stream_t stream) {
+    if (!w) return Q8_ERR_NULL;
+    q8_status st = check_weight_block(w, 1);
+    if (st != Q8_OK) return st;
+    if (m < 0 || m > kMaxBlockDim || k != w->k || ldx < k || ldy < w->n || !block_tiles_fit(m, w->n, 0))
+        return Q8_ERR_SHAPE;
+    if (!float_input(x_dtype)) return Q8_ERR_DTYPE;
+    if (m == 0 || w->n == 0) return Q8_OK;   // empty call
+    if (!X || !Y) return Q8_ERR_NULL;
+    if (!aligned16(X) || !ld_ok(ldx, k, x_dtype) || !aligned16(Y) || ldy % 8 != 0 || (bias && !aligned16(bias)))
+        return Q8_ERR_ALIGN;
+    const size_t need = q8_workspace_size(Q8_OP_LINEAR_FP8_BLOCK, m, w->n, k);
+    if (need > 0 && (!workspace || ws_bytes < need)) return Q8_ERR_WORKSPACE;
+    if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return Q8_ERR_ALIGN;
+    st = check_device();
+    if (st != Q8_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    BlockLinearArgs a = {};
+    a.m = m; a.n = w->n; a.k = k;
+    a.experts = 1;
+    a.w_codes = w->codes; a.ldw = w->ld; a.sw = w->scale;
+    a.bias = bias;
+    a.y = static_cast<__nv_bfloat16*>(Y); a.ldy = ldy;
+    if (m <= kBlockFusedTokens) {
+        a.x = X; a.x_dtype = x_dtype; a.ldx = ldx;
+        return launch_block_linear(a, s);
+    }
+    BlockQuantArgs q = {};
+    q.src = X; q.src_dtype = x_dtype;
+    q.stack = 1; q.rows = m; q.k = k; q.ld = ldx;
+    q.codes = workspace;
+    q.scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + block_codes_bytes(m, k));
+    st = launch_status(launch_block_quant(q, false, s));
+    if (st != Q8_OK) return st;
+    a.x_codes = q.codes; a.sx = q.scale; a.ldx = k;
+    return launch_block_linear(a, s);
+}
+
+q8_status q8_linear_fp8_block_grouped(const q8_act_block* x, const q8_weight_block* w, int64_t num_experts,
+                                      const int32_t* offsets, const float* bias, void* Y, int64_t ldy,
+                                      q8_stream_t stream) {
+    if (!x || !w) return Q8_ERR_NULL;
+    if (num_experts < 1 || num_experts > 512) return Q8_ERR_SHAPE;
+    q8_status st = check_weight_block(w, num_experts);
+    if (st != Q8_OK) return st;
+    const int64_t n = w->n / num_experts;
+    if (x->m < 0 || x->m > kMaxBlockDim || x->k != w->k || x->ld < x->k || ldy < n ||
+        !block_tiles_fit(x->m, n, num_experts))
+        return Q8_ERR_SHAPE;
+    if (x->m == 0 || n == 0) return Q8_OK;   // empty call
+    if (!x->codes || !x->scale || !offsets || !Y) return Q8_ERR_NULL;
+    if (!aligned16(x->codes) || x->ld % 16 != 0 || !aligned16(x->scale) || !aligned16(Y) || ldy % 8 != 0 ||
+        (bias && !aligned16(bias)) || (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return Q8_ERR_ALIGN;
+    st = check_device();
+    if (st != Q8_OK) return st;
+    BlockLinearArgs a = {};
+    a.m = x->m; a.n = n; a.k = w->k;
+    a.x_codes = x->codes; a.sx = x->scale; a.ldx = x->ld;
+    a.experts = num_experts;
+    a.w_codes = w->codes; a.ldw = w->ld; a.sw = w->scale;
+    a.offsets = offsets;
+    a.bias = bias;
+    a.y = static_cast<__nv_bfloat16*>(Y); a.ldy = ldy;
+    return launch_block_linear(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 q8_status q8_get_device_status(int32_t* out, q8_stream_t stream) {

@@ -1,0 +1,936 @@
+// Block-scaled FP8 (e4m3 codes, one scale per 128 values of a token and per
+// 128 x 128 block of a weight): quantizers, the dense linear and the linear
+// grouped by expert.
+//
+//   act     Sx[j, t] = max(fl32(absmax of x[t, 128 j ..] / 448), 1e-8)
+//   weight  Sw[i, j] = the same over rows 128 i .. and columns 128 j ..
+//   linear  y[t, n] = sum_j Sx[j, t] Sw[n / 128, j] p_j,
+//           p_j = sum over the 128 k of group j of qx[t, k] qw[n, k]
+//
+// The scales change along K, so a GEMM cannot leave them to its epilogue:
+// each p_j is one tcgen05 accumulation of 128 values in TMEM, and CUDA cores
+// add it, scaled, to fp32 sums in registers (a "promotion").  TMEM holds two
+// p_j, so the tensor cores work on group j + 1 while group j is promoted.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "q8_block.cuh"
+#include "q8_internal.h"
+#include "q8_tile.cuh"
+
+namespace q8 {
+namespace {
+
+constexpr int kBM = 128;    // MMA M per CTA (TMEM lanes)
+constexpr int kBKB = 128;   // bytes of K per stage: one scale group, one swizzle row
+
+// ============================================================================
+// Quantizers
+// ============================================================================
+//
+// Both read each value once and hold it in registers between the absmax and
+// the codes.  16 lanes share a group of 128 values (16 bytes of a 16-bit type
+// each).
+
+constexpr int kActRows = 32;   // rows per block: the scales of a group leave as one run
+
+// Activation: 32 rows x 256 columns (two groups) per block; a warp takes four
+// rows, 512 bytes of each.  The scales are group-major, so they are gathered
+// in shared memory and written as runs of 32 rows.
+template <typename T>
+__global__ void __launch_bounds__(256)
+act_block_quant_kernel(const T* __restrict__ X, int64_t m, int64_t k, int64_t ldx, uint8_t* __restrict__ codes,
+                       float* __restrict__ scale) {
+    __shared__ float s_sh[2][kActRows];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kActRows;
+    const int64_t col = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+    pdl_wait();
+    pdl_launch_dependents();
+    Eight<T> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = row0 + warp * 4 + i;
+        if (r < m && col < k) v[i].load(X + r * ldx + col);
+        else v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = row0 + warp * 4 + i;
+        float f[8];
+        v[i].values(f);
+        float a = absmax8(f);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const BlockScale s = block_scale(a);
+        if (lane % 16 == 0) s_sh[lane / 16][warp * 4 + i] = s.S;
+        if (r < m && col < k)
+            *reinterpret_cast<uint2*>(codes + r * k + col) =
+                make_uint2(block_codes4(f[0], f[1], f[2], f[3], s), block_codes4(f[4], f[5], f[6], f[7], s));
+    }
+    __syncthreads();
+    if (threadIdx.x < 2 * kActRows) {
+        const int g = threadIdx.x / kActRows, i = threadIdx.x % kActRows;
+        const int64_t j = static_cast<int64_t>(blockIdx.y) * 2 + g;
+        if (j * kBlock < k && row0 + i < m) scale[j * m + row0 + i] = s_sh[g][i];
+    }
+}
+
+// Weight: one 128 x 128 block per CTA, eight passes of 16 rows.  blockIdx.z is
+// the matrix of a stack; its row blocks start anew.
+template <typename T>
+__global__ void __launch_bounds__(256)
+weight_block_quant_kernel(const T* __restrict__ W, int64_t n, int64_t k, int64_t ldw, uint8_t* __restrict__ codes,
+                          float* __restrict__ scale, int64_t nb, int64_t kb) {
+    __shared__ float m_sh[8];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t e = blockIdx.z, bi = blockIdx.y, bj = blockIdx.x;
+    const int64_t col = bj * kBlock + (threadIdx.x % 16) * 8;
+    const int64_t r0 = bi * kBlock + threadIdx.x / 16;
+    Eight<T> v[8];
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 16 * i;
+        if (r < n && col < k) v[i].load(W + (e * n + r) * ldw + col);
+        else v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float f[8];
+        v[i].values(f);
+        a = fmaxf(a, absmax8(f));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if (lane == 0) m_sh[warp] = a;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) a = fmaxf(a, m_sh[w]);
+    const BlockScale s = block_scale(a);
+    if (threadIdx.x == 0) scale[(e * nb + bi) * kb + bj] = s.S;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 16 * i;
+        if (r < n && col < k) {
+            float f[8];
+            v[i].values(f);
+            *reinterpret_cast<uint2*>(codes + (e * n + r) * k + col) =
+                make_uint2(block_codes4(f[0], f[1], f[2], f[3], s), block_codes4(f[4], f[5], f[6], f[7], s));
+        }
+    }
+}
+
+// ============================================================================
+// Pair kernel: 256 x BN tiles on the two SMs of a CTA pair, persistent
+// ============================================================================
+//
+// Roles as in the rowwise pair GEMM (TMA producer, MMA issuer in the even CTA),
+// but eight promotion warps per CTA: a warp reads its 32-lane quarter of TMEM
+// (its threads' token rows) and half of the tile's columns, BN / 2 fp32 sums
+// per thread.  Every K group is handed over through the accumulator barriers,
+// and the sums leave through TMA stores when the tile is done.
+
+constexpr int kPromoWarps = 8;
+constexpr int kPairThreads = 128 + 32 * kPromoWarps;
+// Registers: 384 threads launch with 168 each (64,512); the first warpgroup
+// (TMA, MMA, two idle warps) keeps 72 and the two promotion warpgroups take 216
+// (128 x 72 + 256 x 216 = 64,512), which holds 128 fp32 sums per thread.
+constexpr int kPairRegsLow = 72, kPairRegsHigh = 216;
+
+struct BlockParams {
+    int m, n;
+    const float* sx;      // [kb][m]
+    const float* sw;      // [experts][nb][kb]
+    const float* bias;    // [experts * n] or null
+    __nv_bfloat16* y;
+    int64_t ldy;
+    int* status;
+};
+
+template <int BN>
+struct BlockPairCfg {
+    static constexpr int A_BYTES = kBM * kBKB;
+    static constexpr int B_BYTES = (BN / 2) * kBKB;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int STORE = kPromoWarps * 2 * 2048;   // output staging: two 32 x 32 chunks per warp
+    static constexpr int STAGES_RAW = (227 * 1024 - STORE - 1024 - 6 * 1024) / STAGE;
+    static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int CW = BN / 2;                      // columns per promotion warp
+    static constexpr int SMEM = STAGES * STAGE + STORE + 1024;
+    static_assert(BN == 128 || BN == 256, "a warp's columns lie in one weight block");
+};
+
+template <int BN, bool GROUPED>
+__global__ void __launch_bounds__(kPairThreads, 1)
+gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmY, int use_tmy, const BlockParams p, int num_kb,
+                       int tiles_m, int tiles_n, const int32_t* group_offsets, int experts) {
+    using C = BlockPairCfg<BN>;
+    __shared__ int g_off[GROUPED ? kMaxGroupedExperts + 1 : 1];
+    __shared__ int g_mt[GROUPED ? kMaxGroupedExperts + 1 : 1];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2];
+    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();          // 0: issues the pair's MMAs
+    const int pair = static_cast<int>(blockIdx.x >> 1);
+    const int npairs = static_cast<int>(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], 2 * kPromoWarps);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_sh = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&tmem_base_sh, C::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    if constexpr (GROUPED) {
+        // The routing offsets come from the previous kernels.
+        pdl_wait();
+        if (warp == 2) build_group_map(group_offsets, experts, p.m, 2 * kBM, g_off, g_mt);
+    }
+    tc_fence_before();
+    __syncthreads();
+    // Both CTAs' barriers are initialized before either touches the other's.
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_base_sh;
+    pdl_launch_dependents();
+
+    const int num_tiles = GROUPED ? g_mt[GROUPED ? experts : 0] * tiles_n : tiles_m * tiles_n;
+    auto tile_ref = [&](int tile) -> TileRef {
+        if constexpr (GROUPED) return grouped_tile(tile, g_off, g_mt, experts, 2 * kBM, BN, p.n);
+        else return dense_tile(tile, tiles_m, 2 * kBM, BN, p.m);
+    };
+    if (warp == 0) {
+        reg_dealloc<kPairRegsLow>();
+        // ------------------------------------------------ TMA producer (both CTAs)
+        if (elect_one()) {
+            tma_prefetch_desc(&tmA);
+            tma_prefetch_desc(&tmB);
+            const uint32_t full0 = map_shared_rank(smem_addr(&full_bar[0]), 0);
+            // The weights do not depend on the previous kernel: the first ring
+            // of the first tile's weight halves goes out before the wait.
+            int npre = 0;
+            if constexpr (!GROUPED) {
+                if (pair < num_tiles) {
+                    const TileRef tr0 = tile_ref(pair);
+                    const int yb0 = tr0.b_row + static_cast<int>(rank) * (BN / 2);
+                    npre = num_kb < C::STAGES ? num_kb : C::STAGES;
+                    for (int s = 0; s < npre; ++s) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * C::STAGE);
+                        tma_load_2d_pair(smem + s * C::STAGE + C::A_BYTES, &tmB, full0 + 8u * static_cast<uint32_t>(s),
+                                         s * kBKB, yb0);
+                    }
+                }
+            }
+            pdl_wait();
+            uint32_t issued = (1u << npre) - 1u, last_par = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+                const TileRef tr = tile_ref(tile);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    const bool pre = tile == pair && kb < npre;   // weight half already out
+                    if (!pre && !mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sa = smem + stage * C::STAGE;
+                    if (rank == 0 && !pre) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE);
+                    const uint32_t fb = full0 + 8u * static_cast<uint32_t>(stage);
+                    tma_load_2d_pair(sa, &tmA, fb, kb * kBKB, tr.a_row + static_cast<int>(rank) * kBM);
+                    if (!pre)
+                        tma_load_2d_pair(sa + C::A_BYTES, &tmB, fb, kb * kBKB,
+                                         tr.b_row + static_cast<int>(rank) * (BN / 2));
+                    issued |= 1u << stage;
+                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // Abort: the pair's loads land (on the even CTA's barriers, which
+            // count both CTAs' bytes) before either CTA leaves.
+            if (!ok && rank == 0)
+                for (int s = 0; s < C::STAGES; ++s)
+                    if (issued & (1u << s)) mbar_wait(&full_bar[s], (last_par >> s) & 1, nullptr, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        reg_dealloc<kPairRegsLow>();
+        // ------------------------------------------------ MMA issuer (even CTA)
+        if (rank == 0 && elect_one()) {
+            const uint32_t idesc = make_idesc(1, 0, 0, 2 * kBM, BN);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                        !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + buf * BN;
+                    const uint32_t sa = smem_addr(smem + stage * C::STAGE);
+                    const uint64_t ad = sdesc_kmajor_sw128(sa);
+                    const uint64_t bd = sdesc_kmajor_sw128(sa + C::A_BYTES);
+#pragma unroll
+                    for (int ks = 0; ks < kBKB / 32; ++ks)
+                        mma_issue_pair<kKindF8>(d, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    tc_commit_pair(&tfull_bar[buf], 0x3);
+                    tc_commit_pair(&empty_bar[stage], 0x3);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    buf ^= 1;
+                    if (buf == 0) bphase ^= 1;
+                }
+            }
+            if (!ok) {
+                // Abort: wait for the MMAs already issued before TMEM is freed.
+                tc_commit_pair_local(&drain_bar);
+                mbar_wait(&drain_bar, 0, nullptr, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        reg_dealloc<kPairRegsLow>();
+    } else {
+        reg_alloc<kPairRegsHigh>();
+        // ------------------------------------------------ promotion and epilogue (both CTAs)
+        pdl_wait();
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tempty0 = map_shared_rank(smem_addr(&tempty_bar[0]), 0);
+        uint8_t* store = smem + C::STAGES * C::STAGE + (warp - 4) * 4096;
+        uint32_t sbuf = 0;
+        const int nb_all = (p.n + kBlock - 1) / kBlock;
+        int buf = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+        for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+            const TileRef tr = tile_ref(tile);
+            const int row0 = tr.a_row + static_cast<int>(rank) * kBM + q * 32;
+            const int row = row0 + lane;
+            const int ncol = tr.n_tile + half * C::CW;         // this warp's first column
+            int nb = ncol / kBlock;
+            if (nb >= nb_all) nb = nb_all - 1;                 // columns past n: computed, not stored
+            const int e = GROUPED ? tr.col_off / p.n : 0;
+            const float* sx = p.sx + (row < p.m ? row : p.m - 1);
+            const float* sw = p.sw + (static_cast<int64_t>(e) * nb_all + nb) * num_kb;
+            float2 acc[C::CW / 2];
+#pragma unroll
+            for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            // Scales are fetched four groups ahead of their use.
+            float s_cur[4], s_nxt[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s_cur[j] = j < num_kb ? sx[static_cast<int64_t>(j) * p.m] * sw[j] : 0.f;
+            for (int kb0 = 0; kb0 < num_kb && ok; kb0 += 4) {
+                float a_n[4], b_n[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int kb = kb0 + 4 + j;
+                    a_n[j] = kb < num_kb ? __ldg(sx + static_cast<int64_t>(kb) * p.m) : 0.f;
+                    b_n[j] = kb < num_kb ? __ldg(sw + kb) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (kb0 + j >= num_kb) break;
+                    if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * C::CW;
+                    uint32_t r[2][16];
+                    tmem_ld16(tb, r[0]);
+#pragma unroll
+                    for (int c = 0; c < C::CW / 16; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < C::CW / 16) {
+                            tmem_ld16(tb + (c + 1) * 16, r[(c + 1) & 1]);
+                        } else {
+                            // All of this warp's part is in registers: the buffer may be written again.
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(buf));
+                        }
+                        promote16(acc + c * 8, r[c & 1], s_cur[j]);
+                    }
+                    buf ^= 1;
+                    if (buf == 0) bphase ^= 1;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s_nxt[j] = a_n[j] * b_n[j];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s_cur[j] = s_nxt[j];
+            }
+            if (!ok) break;
+            // A tensor store clips at the output's last row only: chunks that
+            // cross an expert's end are stored row by row.
+            const bool tma = use_tmy && (GROUPED ? row0 + 32 <= tr.row_end : row0 < tr.row_end);
+#pragma unroll
+            for (int c = 0; c < C::CW / 32; ++c) {
+                const int n0 = ncol + c * 32;
+                if (n0 >= p.n) break;                          // uniform over the warp
+                const int nv = (p.n - n0) >= 32 ? 32 : (p.n - n0);   // 16 or 32
+                float out[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    out[2 * i] = acc[c * 16 + i].x;
+                    out[2 * i + 1] = acc[c * 16 + i].y;
+                }
+                if (p.bias) {
+                    const float4* b4 = reinterpret_cast<const float4*>(p.bias + tr.col_off + n0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (4 * i >= nv) break;
+                        const float4 b = __ldg(b4 + i);
+                        out[4 * i] = __fadd_rn(out[4 * i], b.x);
+                        out[4 * i + 1] = __fadd_rn(out[4 * i + 1], b.y);
+                        out[4 * i + 2] = __fadd_rn(out[4 * i + 2], b.z);
+                        out[4 * i + 3] = __fadd_rn(out[4 * i + 3], b.w);
+                    }
+                }
+                if (tma) {
+                    uint8_t* b = store + sbuf * 2048;
+                    if (lane == 0) bulk_wait_read<1>();        // the buffer's previous store has read it
+                    __syncwarp();
+                    const uint32_t sz = static_cast<uint32_t>((lane >> 1) & 3);   // TMA's 64-byte swizzle
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        st_shared_v4(b + lane * 64 + ((static_cast<uint32_t>(j) ^ sz) << 4),
+                                     pack_bf16(out[8 * j], out[8 * j + 1]), pack_bf16(out[8 * j + 2], out[8 * j + 3]),
+                                     pack_bf16(out[8 * j + 4], out[8 * j + 5]), pack_bf16(out[8 * j + 6], out[8 * j + 7]));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmY, b, n0, row0);
+                        bulk_commit();
+                    }
+                    sbuf ^= 1u;
+                } else if (row < tr.row_end) {
+                    uint4* yp = reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.ldy + n0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (8 * j >= nv) break;
+                        yp[j] = make_uint4(pack_bf16(out[8 * j], out[8 * j + 1]), pack_bf16(out[8 * j + 2], out[8 * j + 3]),
+                                           pack_bf16(out[8 * j + 4], out[8 * j + 5]), pack_bf16(out[8 * j + 6], out[8 * j + 7]));
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();   // staged output stores done before the CTA ends
+        __syncwarp();
+    }
+
+    __syncthreads();
+    // No CTA leaves while its partner may still signal one of its barriers or
+    // read its shared memory.
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// ============================================================================
+// Decode kernel: weights as the MMA's M side, tokens as N, split-K in a cluster
+// ============================================================================
+//
+// 128 output channels and up to NT tokens per cluster; the CTAs of a cluster
+// share the K groups and push their fp32 sums to the rank that finishes a
+// token, which adds them in rank order.  With QX the activation arrives
+// unquantized and four more warps quantize each group on its way into the stage (the
+// codes are those of the activation quantizer); without, TMA loads codes.
+//   warp 0 TMA, warp 1 MMA, warps 2-5 promotion and epilogue, warps 6-9 X.
+
+template <int NT, bool QX>
+struct BlockDecodeCfg {
+    static constexpr int THREADS = QX ? 320 : 192;
+    static constexpr int A_BYTES = kBM * kBKB;   // 128 weight rows
+    static constexpr int B_BYTES = NT * kBKB;    // NT token rows
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int RED_BYTES = (NT + 8) * kBM * 4;
+    static constexpr int STAGES_RAW = (227 * 1024 - 1024 - 8 * 1024 - RED_BYTES) / STAGE;
+    static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+    // Scales of quantized-on-the-way groups: a stage is refilled when its MMA
+    // is done, with the promotion at most two groups behind the MMA.
+    static constexpr int SX_RING = STAGES + 2;
+    static constexpr int TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+};
+
+template <int NT, bool QX, typename T>
+__global__ void __launch_bounds__(BlockDecodeCfg<NT, QX>::THREADS, 1)
+gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                         const T* __restrict__ X, int64_t ldx, int k, const BlockParams p, int num_kb,
+                         int kb_per_split, int splits, int nstages) {
+    using C = BlockDecodeCfg<NT, QX>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    float* red = reinterpret_cast<float*>(smem + nstages * C::STAGE);   // [rank][tokens owned][128]
+    __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2];
+    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+    __shared__ __align__(16) float col_s[4][NT];                   // promotion warps: Sx Sw of the group
+    __shared__ float sx_ring[QX ? C::SX_RING : 1][QX ? NT : 1];
+    __shared__ __align__(8) uint64_t sx_bar[QX ? C::SX_RING : 1];  // four quantizing warps have written the slot
+
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const int tn = blockIdx.x;                       // 128 output channels
+    const int t0 = static_cast<int>(blockIdx.z) * NT;
+    const int mt = min(NT, p.m - t0);                // this tile's tokens
+    const uint32_t rank = cluster_ctarank();         // split index along K
+    const int kb0 = static_cast<int>(rank) * kb_per_split;
+    const int kb1 = min(num_kb, kb0 + kb_per_split);
+    const int my_kb = kb1 > kb0 ? kb1 - kb0 : 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < nstages; ++s) {
+            mbar_init(&full_bar[s], QX ? 5 : 1);     // TMA (and the four quantizing warps)
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], 4);
+        }
+        if constexpr (QX)
+            for (int s = 0; s < C::SX_RING; ++s) mbar_init(&sx_bar[s], 4);
+        mbar_init(&drain_bar, 1);
+        abort_sh = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_base_sh;
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        if (elect_one()) {
+            constexpr uint32_t kBytes = QX ? C::A_BYTES : C::STAGE;
+            tma_prefetch_desc(&tmW);
+            if constexpr (!QX) tma_prefetch_desc(&tmX);
+            // The weights do not depend on the previous kernel: their first
+            // ring goes out before the programmatic-launch wait.
+            const int first = my_kb < nstages ? my_kb : nstages;
+            for (int i = 0; i < first; ++i) {
+                mbar_arrive_expect_tx(&full_bar[i], kBytes);
+                tma_load_2d(smem + i * C::STAGE, &tmW, &full_bar[i], (kb0 + i) * kBKB, tn * kBM);
+            }
+            if constexpr (!QX) {
+                pdl_wait();
+                for (int i = 0; i < first; ++i)
+                    tma_load_2d(smem + i * C::STAGE + C::A_BYTES, &tmX, &full_bar[i], (kb0 + i) * kBKB, t0);
+            }
+            uint32_t issued = (1u << first) - 1u, last_par = 0;
+            int stage = first == nstages ? 0 : first;
+            uint32_t phase = first == nstages ? 1u : 0u;
+            bool ok = true;
+            for (int kb = kb0 + first; kb < kb1; ++kb) {
+                if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* sa = smem + stage * C::STAGE;
+                mbar_arrive_expect_tx(&full_bar[stage], kBytes);
+                tma_load_2d(sa, &tmW, &full_bar[stage], kb * kBKB, tn * kBM);
+                if constexpr (!QX) tma_load_2d(sa + C::A_BYTES, &tmX, &full_bar[stage], kb * kBKB, t0);
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == nstages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok)   // the loads already issued land before the CTA leaves
+                for (int s = 0; s < nstages; ++s)
+                    if (issued & (1u << s)) mbar_wait(&full_bar[s], (last_par >> s) & 1, nullptr, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((mt + 15) / 16 * 16));
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int i = 0; i < my_kb; ++i) {
+                if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                    !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_addr(smem + stage * C::STAGE);
+                const uint64_t ad = sdesc_kmajor_sw128(sa);
+                const uint64_t bd = sdesc_kmajor_sw128(sa + C::A_BYTES);
+#pragma unroll
+                for (int ks = 0; ks < kBKB / 32; ++ks)
+                    mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                tc_commit(&tfull_bar[buf]);
+                tc_commit(&empty_bar[stage]);
+                if (++stage == nstages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1;
+            }
+            if (!ok) {
+                tc_commit(&drain_bar);
+                mbar_wait(&drain_bar, 0, nullptr, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        const int q = warp & 3;
+        const int ch = q * 32 + lane;
+        const int tpo = (NT + splits - 1) / splits;     // tokens owned per rank
+        const float* sw = p.sw + static_cast<int64_t>(tn) * num_kb;
+        float* cs = col_s[q];
+        float2 acc[NT / 2];
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+        if constexpr (!QX) pdl_wait();
+        int buf = 0;
+        uint32_t bphase = 0;
+        for (int i = 0; i < my_kb; ++i) {
+            const int kb = kb0 + i;
+            const float swk = __ldg(sw + kb);
+            if constexpr (!QX) {
+#pragma unroll
+                for (int c = 0; c < NT; c += 32) {
+                    const int t = c + lane;
+                    if (t < NT) cs[t] = t < mt ? p.sx[static_cast<int64_t>(kb) * p.m + t0 + t] * swk : 0.f;
+                }
+            }
+            if constexpr (QX) {
+                if (!mbar_wait(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
+#pragma unroll
+                for (int c = 0; c < NT; c += 32) {
+                    const int t = c + lane;
+                    if (t < NT) cs[t] = t < mt ? sx_ring[i % C::SX_RING][t] * swk : 0.f;
+                }
+            }
+            if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                if (c * 16 < mt) {
+                    uint32_t r[16];
+                    tmem_ld16(tb + c * 16, r);
+                    tmem_ld_wait();
+                    promote16(acc + c * 8, r, cs + c * 16);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+            buf ^= 1;
+            if (buf == 0) bphase ^= 1;
+        }
+        const uint32_t red_base = smem_addr(red);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t < mt) {
+                const float v = (t & 1) ? acc[t / 2].y : acc[t / 2].x;
+                const uint32_t off = ((rank * tpo + t / splits) * kBM + ch) * 4u;
+                st_shared_cluster_u32(map_shared_rank(red_base + off, static_cast<uint32_t>(t % splits)),
+                                      __float_as_uint(v));
+            }
+        }
+        __syncwarp();
+    } else if constexpr (QX) {
+        // Quantizing warps: 8 lanes per token, 16 tokens per pass of the four warps.
+        pdl_wait();
+        const int qw = warp - 6;
+        const int sub = lane & 7;                       // 16-value piece of the group
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < my_kb; ++i) {
+            const int kb = kb0 + i;
+            Eight<T> lo[NT / 16], hi[NT / 16];
+            const int col = kb * kBlock + sub * 16;
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                const int t = c * 16 + qw * 4 + lane / 8;
+                lo[c].zero();
+                hi[c].zero();
+                if (t < mt && col < k) {
+                    const T* src = X + static_cast<int64_t>(t0 + t) * ldx + col;
+                    lo[c].load(src);
+                    hi[c].load(src + 8);
+                }
+            }
+            if (i >= nstages && !mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) break;
+            __syncwarp();
+            uint8_t* sb = smem + stage * C::STAGE + C::A_BYTES;
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                const int t = c * 16 + qw * 4 + lane / 8;
+                if (c * 16 < mt) {                      // uniform over the warp
+                    float s;
+                    const uint4 w = quantize16<T>(lo[c], hi[c], s);
+                    st_shared_v4(sb + t * kBKB + ((sub ^ (t & 7)) << 4), w.x, w.y, w.z, w.w);
+                    if (sub == 0) sx_ring[i % C::SX_RING][t] = s;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&full_bar[stage]);
+                mbar_arrive(&sx_bar[i % C::SX_RING]);
+            }
+            if (++stage == nstages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        __syncwarp();
+    }
+
+    // Every rank's pushed sums are visible after this barrier; after it no CTA
+    // touches another CTA's shared memory, so each may exit when done.
+    __syncthreads();
+    cluster_sync();
+
+    if (warp >= 2 && warp < 6) {
+        const int ch = (warp & 3) * 32 + lane;
+        const int tpo = (NT + splits - 1) / splits;
+        const int n = tn * kBM + ch;
+        if constexpr (QX) pdl_wait();   // Y may still be read by the previous kernel
+        if (n < p.n && !abort_sh) {
+            const float bias = p.bias ? p.bias[n] : 0.f;
+            for (int t = static_cast<int>(rank); t < mt; t += splits) {
+                float s = 0.f;
+                for (int r = 0; r < splits; ++r) s = __fadd_rn(s, red[(r * tpo + t / splits) * kBM + ch]);
+                if (p.bias) s = __fadd_rn(s, bias);
+                p.y[static_cast<int64_t>(t0 + t) * p.ldy + n] = __float2bfloat16_rn(s);
+            }
+        }
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// ============================================================================
+// Host side
+// ============================================================================
+template <typename T>
+cudaError_t act_quant(const BlockQuantArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kActRows - 1) / kActRows), static_cast<unsigned>((a.k + 255) / 256), 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, act_block_quant_kernel<T>, static_cast<const T*>(a.src), a.rows, a.k, a.ld,
+                              static_cast<uint8_t*>(a.codes), a.scale);
+}
+
+template <typename T>
+cudaError_t weight_quant(const BlockQuantArgs& a, cudaStream_t s) {
+    const int64_t nb = (a.rows + kBlock - 1) / kBlock, kb = (a.k + kBlock - 1) / kBlock;
+    weight_block_quant_kernel<T><<<dim3(static_cast<unsigned>(kb), static_cast<unsigned>(nb), static_cast<unsigned>(a.stack)),
+                                   256, 0, s>>>(static_cast<const T*>(a.src), a.rows, a.k, a.ld,
+                                                static_cast<uint8_t*>(a.codes), a.scale, nb, kb);
+    return cudaGetLastError();
+}
+
+BlockParams block_params(const BlockLinearArgs& a) {
+    BlockParams p = {};
+    p.m = static_cast<int>(a.m);
+    p.n = static_cast<int>(a.n);
+    p.sx = a.sx;
+    p.sw = a.sw;
+    p.bias = a.bias;
+    p.y = a.y;
+    p.ldy = a.ldy;
+    p.status = device_status_ptr();
+    return p;
+}
+
+template <int BN, bool GROUPED>
+q8_status run_block_pair(const BlockLinearArgs& a, cudaStream_t s) {
+    using C = BlockPairCfg<BN>;
+    CUtensorMap tA, tB, tY;
+    if (!make_map(&tA, a.x_codes, false, a.k, a.m, a.ldx, kBKB, kBM) ||
+        !make_map(&tB, a.w_codes, false, a.k, a.experts * a.n, a.ldw, kBKB, BN / 2))
+        return Q8_ERR_CUDA;
+    const int use_tmy = make_map_y(&tY, a.y, a.n, a.m, a.ldy) ? 1 : 0;
+    if (!use_tmy) tY = tA;
+    auto kern = gemm_block_pair_kernel<BN, GROUPED>;
+    if (set_smem(kern, C::SMEM) != cudaSuccess) return Q8_ERR_LAUNCH;
+    const int tiles_n = static_cast<int>((a.n + BN - 1) / BN);
+    const int tiles_m = static_cast<int>((a.m + 2 * kBM - 1) / (2 * kBM));
+    // Grouped: an upper bound (each expert adds at most one partial row tile);
+    // the kernel reads the offsets and walks the actual tiles.
+    const int64_t tiles = (tiles_m + (GROUPED ? a.experts : 0)) * tiles_n;
+    const int pairs_max = max_pairs(kern, C::SMEM, kPairThreads);
+    const int pairs = static_cast<int>(tiles < pairs_max ? tiles : pairs_max);
+    const int num_kb = static_cast<int>((a.k + kBKB - 1) / kBKB);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, tA, tB, tY, use_tmy, block_params(a), num_kb, tiles_m, tiles_n, a.offsets,
+                           static_cast<int>(a.experts)) != cudaSuccess) {
+        cudaGetLastError();
+        return Q8_ERR_LAUNCH;
+    }
+    return Q8_OK;
+}
+
+template <int NT, bool QX, typename T>
+q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
+    using C = BlockDecodeCfg<NT, QX>;
+    CUtensorMap tW, tX;
+    if (!make_map(&tW, a.w_codes, false, a.k, a.n, a.ldw, kBKB, kBM)) return Q8_ERR_CUDA;
+    if (QX) tX = tW;
+    else if (!make_map(&tX, a.x_codes, false, a.k, a.m, a.ldx, kBKB, NT)) return Q8_ERR_CUDA;
+    auto kern = gemm_block_decode_kernel<NT, QX, T>;
+    const int tiles_n = static_cast<int>((a.n + kBM - 1) / kBM);
+    const int tiles_t = static_cast<int>((a.m + NT - 1) / NT);
+    const int num_kb = static_cast<int>((a.k + kBKB - 1) / kBKB);
+    // Split K across the CTAs of a cluster (at most 8, every split non-empty)
+    // so that the grid fills the SMs at two CTAs per SM, which the short stage
+    // ring of a split allows.
+    int want = 2 * sm_count() / (tiles_n * tiles_t);
+    if (want < 1) want = 1;
+    if (want > 8) want = 8;
+    if (want > num_kb) want = num_kb;
+    const int per = (num_kb + want - 1) / want;
+    const int splits = (num_kb + per - 1) / per;
+    const int nstages = per < C::STAGES ? per : C::STAGES;
+    const int smem = nstages * C::STAGE + C::RED_BYTES + 1024;
+    if (set_smem(kern, smem) != cudaSuccess) return Q8_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles_n), static_cast<unsigned>(splits), static_cast<unsigned>(tiles_t));
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, tW, tX, static_cast<const T*>(a.x), a.ldx, static_cast<int>(a.k),
+                           block_params(a), num_kb, per, splits, nstages) != cudaSuccess) {
+        cudaGetLastError();
+        return Q8_ERR_LAUNCH;
+    }
+    return Q8_OK;
+}
+
+template <typename T>
+q8_status run_fused(const BlockLinearArgs& a, cudaStream_t s) {
+    if (a.m <= 16) return run_block_decode<16, true, T>(a, s);
+    if (a.m <= 32) return run_block_decode<32, true, T>(a, s);
+    return run_block_decode<64, true, T>(a, s);
+}
+
+// Tile width of the pair kernel: the persistent grid's makespan, waves x (BN +
+// a tile's fixed cost of about 64 columns' worth), the wider tile on ties.
+bool wide_tiles(int64_t row_tiles, int64_t n) {
+    const int64_t pairs = sm_count() / 2;
+    auto cost = [&](int64_t bn) {
+        const int64_t tiles = row_tiles * ((n + bn - 1) / bn);
+        return ((tiles + pairs - 1) / pairs) * (bn + 64);
+    };
+    return cost(256) <= cost(128);
+}
+
+}  // namespace
+
+cudaError_t launch_block_quant(const BlockQuantArgs& a, bool weight, cudaStream_t s) {
+    switch (a.src_dtype) {
+        case Q8_F16: return weight ? weight_quant<__half>(a, s) : act_quant<__half>(a, s);
+        case Q8_BF16: return weight ? weight_quant<__nv_bfloat16>(a, s) : act_quant<__nv_bfloat16>(a, s);
+        default: return weight ? weight_quant<float>(a, s) : act_quant<float>(a, s);
+    }
+}
+
+q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
+    if (a.offsets) {
+        const int64_t rows = (a.m + 2 * kBM - 1) / (2 * kBM) + a.experts / 2;
+        return wide_tiles(rows, a.n) ? run_block_pair<256, true>(a, s) : run_block_pair<128, true>(a, s);
+    }
+    if (a.x) {   // quantized on the way
+        switch (a.x_dtype) {
+            case Q8_F16: return run_fused<__half>(a, s);
+            case Q8_BF16: return run_fused<__nv_bfloat16>(a, s);
+            default: return run_fused<float>(a, s);
+        }
+    }
+    if (a.m <= 16) return run_block_decode<16, false, __half>(a, s);
+    if (a.m <= 32) return run_block_decode<32, false, __half>(a, s);
+    if (a.m <= 64) return run_block_decode<64, false, __half>(a, s);
+    if (a.m <= 2 * kBM) return run_block_decode<128, false, __half>(a, s);
+    return wide_tiles((a.m + 2 * kBM - 1) / (2 * kBM), a.n) ? run_block_pair<256, false>(a, s)
+                                                            : run_block_pair<128, false>(a, s);
+}
+
+}  // namespace q8

@@ -125,5 +125,33 @@ q8_status launch_moe_fp8(const MoeArgs& a, cudaStream_t s);
 // Q8_ERR_SHAPE for more experts than its tile map holds.
 q8_status launch_grouped_fp8(const MoeArgs& a, cudaStream_t s);
 
+// ---- block-scaled FP8 (q8_block.cu)
+struct BlockQuantArgs {
+    const void* src;                       // stack * rows x k (f16 / bf16 / f32), row stride ld elements
+    q8_dtype src_dtype;
+    int64_t stack, rows, k, ld;            // activations: stack = 1
+    void* codes;                           // row stride k
+    float* scale;                          // act: [ceil(k/128)][rows]; weight: [stack][ceil(rows/128)][ceil(k/128)]
+};
+
+cudaError_t launch_block_quant(const BlockQuantArgs& a, bool weight, cudaStream_t s);
+
+struct BlockLinearArgs {
+    int64_t m, n, k;
+    const void* x; q8_dtype x_dtype;       // activation quantized on the way (m <= kBlockFusedTokens), or null
+    const void* x_codes; const float* sx;  // else codes m x k and scales [ceil(k/128)][m]
+    int64_t ldx;                           // row stride of x or x_codes, elements
+    int64_t experts;                       // 1, or the experts of a grouped call
+    const void* w_codes; int64_t ldw;      // experts * n x k
+    const float* sw;                       // [experts][ceil(n/128)][ceil(k/128)]
+    const int32_t* offsets;                // grouped: device [experts + 1], else null
+    const float* bias;                     // [experts * n] or null
+    __nv_bfloat16* y; int64_t ldy;
+};
+
+// Tokens up to which a dynamic call quantizes inside the GEMM.
+constexpr int64_t kBlockFusedTokens = 64;
+
+q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s);
 
 }  // namespace q8

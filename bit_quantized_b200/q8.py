@@ -32,7 +32,7 @@ Q8_OK, Q8_ERR_NULL, Q8_ERR_SHAPE, Q8_ERR_ALIGN, Q8_ERR_DTYPE, Q8_ERR_SCHEME = ra
 Q8_ERR_UNSUPPORTED_ARCH, Q8_ERR_LAUNCH, Q8_ERR_DEVICE_TIMEOUT, Q8_ERR_WORKSPACE, Q8_ERR_CUDA = range(6, 11)
 Q8_S8, Q8_U8, Q8_E4M3, Q8_F16, Q8_BF16, Q8_F32, Q8_S32 = range(7)
 Q8_ASYM_INT8, Q8_SYM_INT8, Q8_FP8_E4M3 = range(3)
-Q8_OP_LINEAR_W8A8, Q8_OP_LINEAR_INT8_MIXED = 0, 1
+Q8_OP_LINEAR_W8A8, Q8_OP_LINEAR_INT8_MIXED, Q8_OP_LINEAR_FP8_BLOCK = 0, 1, 2
 Q8_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTED = [
@@ -43,6 +43,8 @@ EXPORTED = [
     "q8_linear_int8_mixed_noalloc",
     "q8_quantize_weight_g4", "q8_quantize_weight_q4k", "q8_expand_q4k_scales", "q8_linear_w4a16",
     "q8_linear_fp8_grouped",
+    "q8_quantize_act_block", "q8_quantize_weight_block",
+    "q8_linear_fp8_block", "q8_linear_fp8_block_dynamic", "q8_linear_fp8_block_grouped",
     "q8_workspace_size", "q8_status_string",
     "q8_get_device_status", "q8_clear_device_status", "q8_device_check", "q8_version",
     "q8_inject_failure", "q8_selftest_wait_timeout",
@@ -65,6 +67,16 @@ class CWeightG4(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("ld", ctypes.c_int64),
                 ("group", ctypes.c_int32)]
+
+
+class CWeightBlock(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("ld", ctypes.c_int64)]
+
+
+class CActBlock(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("m", ctypes.c_int64), ("k", ctypes.c_int64), ("ld", ctypes.c_int64)]
 
 
 _i64, _int, _f, _vp, _sz = ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
@@ -94,6 +106,14 @@ _SIG = {
                                _i64, _vp], _int),
     "q8_linear_w4a16": ([_vp, _int, _i64, _i64, _i64, ctypes.POINTER(CWeightG4), _vp, _vp, _i64,
                          _vp], _int),
+    "q8_quantize_act_block": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "q8_quantize_weight_block": ([_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "q8_linear_fp8_block": ([ctypes.POINTER(CActBlock), ctypes.POINTER(CWeightBlock), _vp, _vp,
+                             _i64, _vp], _int),
+    "q8_linear_fp8_block_dynamic": ([_vp, _int, _i64, _i64, _i64, ctypes.POINTER(CWeightBlock),
+                                     _vp, _vp, _i64, _vp, _sz, _vp], _int),
+    "q8_linear_fp8_block_grouped": ([ctypes.POINTER(CActBlock), ctypes.POINTER(CWeightBlock), _i64,
+                                     _vp, _vp, _vp, _i64, _vp], _int),
     "q8_workspace_size": ([_int, _i64, _i64, _i64], _sz),
     "q8_status_string": ([_int], ctypes.c_char_p),
     "q8_get_device_status": ([_vp, _vp], _int),
@@ -483,6 +503,198 @@ def q8_linear_fp8_grouped(x: QAct, w: QWeight, num_experts: int, offsets: torch.
     _check(_lib.q8_linear_fp8_grouped(ctypes.byref(cx), ctypes.byref(cw), int(num_experts),
                                       _ptr(offsets.contiguous()), _ptr(bias), _ptr(out),
                                       out.stride(0), _stream(stream)), "q8_linear_fp8_grouped")
+    return out
+
+
+# ---------------------------------------------------------------- block-scaled FP8
+#
+# These calls run on the device of their first tensor (made current for the
+# call) and on that device's current torch stream unless `stream` names
+# another.  Outputs and workspaces allocated here for another stream are
+# recorded on it, so that their memory is not reused under the kernels.
+
+@dataclasses.dataclass
+class QWeightBlock:
+    """A block-scaled FP8 weight (device tensors): codes n x k float8_e4m3fn, scale
+    ceil(n/128) x ceil(k/128) fp32; a stack of experts has codes experts x n x k and
+    scale experts x ceil(n/128) x ceil(k/128)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def experts(self) -> int:
+        return self.codes.shape[0] if self.codes.dim() == 3 else 1
+
+    def c(self) -> CWeightBlock:
+        q, S = self.codes, self.scale
+        n, k = q.shape[-2:]
+        if q.dim() not in (2, 3) or not q.is_cuda or q.dtype != torch.float8_e4m3fn or q.stride(-1) != 1:
+            raise ValueError("weight codes must be a 2-D or 3-D CUDA float8_e4m3fn tensor with unit column stride")
+        if q.dim() == 3 and q.shape[0] > 1 and q.stride(0) != n * q.stride(1):
+            raise ValueError("the experts of a weight stack must follow each other without a gap")
+        want = q.shape[:-2] + ((n + 127) // 128, (k + 127) // 128)
+        if S.device != q.device or S.dtype != torch.float32 or S.shape != want or not S.is_contiguous():
+            raise ValueError(f"weight scale must be a contiguous float32 tensor of shape {tuple(want)} on the codes' device")
+        return CWeightBlock(q.data_ptr(), S.data_ptr(), self.experts * n, k, q.stride(-2))
+
+
+@dataclasses.dataclass
+class QActBlock:
+    """A block-scaled FP8 activation (device tensors): codes m x k float8_e4m3fn, scale
+    ceil(k/128) x m fp32 (group-major)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    def c(self) -> CActBlock:
+        q, S = self.codes, self.scale
+        if q.dim() != 2 or not q.is_cuda or q.dtype != torch.float8_e4m3fn or q.stride(1) != 1:
+            raise ValueError("activation codes must be a 2-D CUDA float8_e4m3fn tensor with unit column stride")
+        m, k = q.shape
+        if S.device != q.device or S.dtype != torch.float32 or S.shape != ((k + 127) // 128, m) or not S.is_contiguous():
+            raise ValueError(f"activation scale must be a contiguous float32 tensor of shape {((k + 127) // 128, m)} "
+                             "on the codes' device")
+        return CActBlock(q.data_ptr(), S.data_ptr(), m, k, q.stride(0))
+
+
+def _on(device, call, made, stream, where, args, others=()):
+    """Runs a C entry point with `device` current, on its stream; `made` tensors were allocated for the call."""
+    for t, name in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+    index = device.index
+    if index == torch.cuda.current_device():
+        return _launch(device, call, made, stream, where, args)
+    with torch.cuda.device(index):
+        return _launch(device, call, made, stream, where, args)
+
+
+def _launch(device, call, made, stream, where, args):
+    own = torch.cuda.current_stream(device)
+    s = own if stream is None else stream
+    if s.device != device:
+        raise ValueError(f"the stream must belong to {device}")
+    _check(call(*args, s.cuda_stream), where)
+    if s.cuda_stream != own.cuda_stream:
+        for t in made:
+            t.record_stream(s)
+
+
+def _check_out(out, shape, dtype, device, name="out"):
+    if out.device != device or out.dtype != dtype or out.shape != shape or (out.shape[-1] > 1 and out.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with unit column stride on {device}")
+    return out
+
+
+def _ld(t: torch.Tensor) -> int:
+    # The stride of a single row means nothing to torch: the row's length stands for it.
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _check_bias(bias, n, device):
+    if bias is not None and (bias.device != device or bias.dtype != torch.float32 or bias.numel() != n
+                             or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous float32 tensor of {n} values on {device}")
+
+
+def q8_quantize_act_block(X: torch.Tensor, out: Optional[QActBlock] = None, stream=None) -> QActBlock:
+    """FP8 codes with one scale per token and 128 values (see q8_quantize_act_block in q8.h)."""
+    _cuda(X, "X")
+    m, k = X.shape
+    made = ()
+    if out is None:
+        out = QActBlock(torch.empty((m, k), dtype=torch.float8_e4m3fn, device=X.device),
+                        torch.empty(((k + 127) // 128, m), dtype=torch.float32, device=X.device))
+        made = (out.codes, out.scale)
+    else:
+        out.c()
+        _check_out(out.codes, (m, k), torch.float8_e4m3fn, X.device, "out.codes")
+        if not out.codes.is_contiguous():
+            raise ValueError("out.codes must be contiguous")
+    _on(X.device, _lib.q8_quantize_act_block, made, stream, "q8_quantize_act_block",
+        (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, k, _ld(X), out.codes.data_ptr(), out.scale.data_ptr()))
+    return out
+
+
+def q8_quantize_weight_block(W: torch.Tensor, stream=None) -> QWeightBlock:
+    """FP8 codes with one scale per 128 x 128 block; W is n x k, or a stack experts x n x k."""
+    stack = W.dim() == 3
+    if stack and not W.is_contiguous():
+        raise ValueError("a stack of weights must be contiguous")
+    e = W.shape[0] if stack else 1
+    W2 = _cuda(W.reshape(-1, W.shape[-1]) if stack else W, "W")
+    n, k = W.shape[-2:]
+    shape = (((n + 127) // 128), (k + 127) // 128)
+    q = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=W.device)
+    S = torch.empty((e, *shape) if stack else shape, dtype=torch.float32, device=W.device)
+    _on(W.device, _lib.q8_quantize_weight_block, (q, S), stream, "q8_quantize_weight_block",
+        (W2.data_ptr(), _FLOAT_DT.get(W.dtype, -1), e, n, k, _ld(W2), q.data_ptr(), S.data_ptr()))
+    return QWeightBlock(q, S)
+
+
+def q8_linear_fp8_block(x: QActBlock, w: QWeightBlock, bias: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Block-scaled FP8 linear of a quantized activation; returns bf16 m x n."""
+    cx, cw = x.c(), w.c()
+    dev = x.codes.device
+    made = ()
+    if out is None:
+        out = torch.empty((cx.m, cw.n), dtype=torch.bfloat16, device=dev)
+        made = (out,)
+    else:
+        _check_out(out, (cx.m, cw.n), torch.bfloat16, dev)
+    _check_bias(bias, cw.n, dev)
+    _on(dev, _lib.q8_linear_fp8_block, made, stream, "q8_linear_fp8_block",
+        (ctypes.byref(cx), ctypes.byref(cw), _ptr(bias), out.data_ptr(), _ld(out)), ((w.codes, "w"),))
+    return out
+
+
+def q8_linear_fp8_block_dynamic(X: torch.Tensor, w: QWeightBlock, bias: Optional[torch.Tensor] = None,
+                                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """Activation quantization and block-scaled FP8 linear in one call; returns bf16 m x n."""
+    _cuda(X, "X")
+    m, k = X.shape
+    cw = w.c()
+    dev = X.device
+    made = []
+    if out is None:
+        out = torch.empty((m, cw.n), dtype=torch.bfloat16, device=dev)
+        made.append(out)
+    else:
+        _check_out(out, (m, cw.n), torch.bfloat16, dev)
+    need = q8_workspace_size(Q8_OP_LINEAR_FP8_BLOCK, m, cw.n, k)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _check_bias(bias, cw.n, dev)
+    _on(dev, _lib.q8_linear_fp8_block_dynamic, made, stream, "q8_linear_fp8_block_dynamic",
+        (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, k, _ld(X), ctypes.byref(cw), _ptr(bias), out.data_ptr(), _ld(out),
+         _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()),
+        ((w.codes, "w"), (workspace, "workspace")))
+    return out
+
+
+def q8_linear_fp8_block_grouped(x: QActBlock, w: QWeightBlock, offsets: torch.Tensor,
+                                bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """Grouped block-scaled FP8 linear (mixture of experts): tokens sorted by expert, w a stack of
+    experts, offsets a CUDA int32 tensor of experts + 1 entries; returns bf16 m x n."""
+    cx, cw = x.c(), w.c()
+    e = w.experts
+    dev = x.codes.device
+    if offsets.device != dev or offsets.dtype != torch.int32 or offsets.shape != (e + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {e + 1} entries on {dev}")
+    n = cw.n // max(e, 1)
+    made = ()
+    if out is None:
+        out = torch.empty((cx.m, n), dtype=torch.bfloat16, device=dev)
+        made = (out,)
+    else:
+        _check_out(out, (cx.m, n), torch.bfloat16, dev)
+    _check_bias(bias, cw.n, dev)
+    _on(dev, _lib.q8_linear_fp8_block_grouped, made, stream, "q8_linear_fp8_block_grouped",
+        (ctypes.byref(cx), ctypes.byref(cw), e, offsets.data_ptr(), _ptr(bias), out.data_ptr(), _ld(out)),
+        ((w.codes, "w"),))
     return out
 
 

@@ -13,7 +13,9 @@
  *   - group-wise 4-bit weights with one absmax scale per group of 32-128
  *     values along K (optionally with GGUF Q4_K-style quantized group scales),
  *     multiplied with 16-bit activations (W4A16);
- *   - the grouped FP8 rowwise linear of mixture-of-experts layers.
+ *   - the grouped FP8 rowwise linear of mixture-of-experts layers;
+ *   - block-scaled FP8 (one scale per 128 values of a token and per 128 x 128
+ *     block of a weight): quantizers, linear, grouped linear.
  *
  * Notation follows the pages' linear map Q = round(R / S) + Z, R = S (Q - Z):
  * `scale` is S, the dequant multiplier, and `zero_point` is Z, an integer held
@@ -66,7 +68,7 @@
 extern "C" {
 #endif
 
-#define Q8_VERSION 8
+#define Q8_VERSION 9
 
 /* Same object as cudaStream_t. */
 typedef struct CUstream_st *q8_stream_t;
@@ -500,13 +502,99 @@ q8_status q8_linear_int8_mixed_noalloc(const void *X, q8_dtype x_dtype, int64_t 
                                        int32_t *acc_debug, float *y16_debug,
                                        q8_stream_t stream);
 
-enum { Q8_OP_LINEAR_W8A8 = 0, Q8_OP_LINEAR_INT8_MIXED = 1 };
+/* A block-scaled FP8 weight: E4M3 codes (row stride `ld` elements) with one
+ * fp32 scale per block of 128 rows and 128 columns ([CSDN] 2.2 granularity
+ * table: smaller groups follow the local range of a weight; 128 x 128 blocks
+ * with 1 x 128 activation groups are the format of block-wise FP8
+ * checkpoints).  A stack of experts' weights is one q8_weight_block with
+ * n = experts * (rows of one expert); row blocks start anew in every expert.
+ *   scale   [experts][ceil(rows / 128)][ceil(k / 128)], dense. */
+typedef struct {
+    const void *codes;
+    const float *scale;
+    int64_t n, k, ld;
+} q8_weight_block;
+
+/* A block-scaled FP8 activation: m x k E4M3 codes with one fp32 scale per
+ * token and 128 consecutive values.
+ *   scale   [ceil(k / 128)][m], group-major and dense: scale[j * m + t]. */
+typedef struct {
+    const void *codes;
+    const float *scale;
+    int64_t m, k, ld;
+} q8_act_block;
+
+/*
+ * Block-scaled FP8 quantization.  For every group (activation: 128
+ * consecutive values of a token; weight: 128 x 128 values of a matrix; the
+ * last ones may be smaller) S = max(fl32(absmax / 448), 1e-8) and
+ * q = e4m3_rne_satfinite(fl32(x / S)), bit-exact with a scalar reference.
+ *   X / W    device, Q8_F16, Q8_BF16 or Q8_F32, row stride ldx / ldw.
+ *   experts  matrices of n rows each, stacked (1 for a single weight, at most
+ *            65535; experts * n <= 2^31 - 1).
+ *   codes    device output, row stride k.
+ *   scale    device output, the layouts above.
+ * m, n, k <= 65535 * 128.  One launch each; the weight quantizer does not
+ * trigger an early launch (the launch-overlap rule of q8_linear_w8a8).
+ */
+q8_status q8_quantize_act_block(const void *X, q8_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                void *codes, float *scale, q8_stream_t stream);
+
+q8_status q8_quantize_weight_block(const void *W, q8_dtype w_dtype, int64_t experts, int64_t n,
+                                   int64_t k, int64_t ldw, void *codes, float *scale,
+                                   q8_stream_t stream);
+
+/*
+ * Block-scaled FP8 linear, bf16 out.  With group j of K (128 values):
+ *   p[j] = sum_{k in j} e4m3(xq[m, k]) e4m3(wq[n, k])      (tensor cores, fp32)
+ *   y = sum_j fl32(Sx[j, m] * Sw[n / 128, j]) * p[j]       (fp32 sums, FMA)
+ *   y = fl32(y + bias[n]);  Y[m, n] = bf16_rne(y)
+ * The order of the fp32 sums is not specified, but the same for every call
+ * with the same sizes (results repeat bit for bit).
+ *   x       x->k == w->k;  m <= 65535 * 128.
+ *   bias    device [n] fp32, or NULL.
+ *   Y       device, m x n bf16, row stride ldy >= n, ldy % 8 == 0.
+ * The dynamic form takes the unquantized activation and gives the result of
+ * q8_quantize_act_block followed by q8_linear_fp8_block; up to 64 tokens it
+ * quantizes inside the GEMM (one launch, no workspace), above that into the
+ * workspace (two launches).
+ *   X          device, Q8_F16, Q8_BF16 or Q8_F32, row stride ldx.
+ *   workspace  at least q8_workspace_size(Q8_OP_LINEAR_FP8_BLOCK, m, n, k)
+ *              bytes (0 up to 64 tokens), 256-byte aligned; needs no
+ *              initialization.  Calls that overlap on the GPU need one each.
+ * The launch-overlap rule of q8_linear_w8a8 applies to codes and scales of
+ * the weight.
+ */
+q8_status q8_linear_fp8_block(const q8_act_block *x, const q8_weight_block *w, const float *bias,
+                              void *Y, int64_t ldy, q8_stream_t stream);
+
+q8_status q8_linear_fp8_block_dynamic(const void *X, q8_dtype x_dtype, int64_t m, int64_t k,
+                                      int64_t ldx, const q8_weight_block *w, const float *bias,
+                                      void *Y, int64_t ldy, void *workspace, size_t ws_bytes,
+                                      q8_stream_t stream);
+
+/*
+ * Grouped block-scaled FP8 linear of a mixture-of-experts layer: as
+ * q8_linear_fp8_grouped (tokens sorted by expert, device offsets), with the
+ * block-scaled operands and sums of q8_linear_fp8_block.
+ *   num_experts  1 .. 512; w->n = num_experts * n, n % 16 == 0.
+ *   offsets      device int32 [num_experts + 1], as q8_linear_fp8_grouped
+ *                (clamped to [0, x->m] and made non-decreasing; rows that no
+ *                expert covers are left unwritten).
+ *   bias         device fp32 [num_experts * n], or NULL.
+ */
+q8_status q8_linear_fp8_block_grouped(const q8_act_block *x, const q8_weight_block *w,
+                                      int64_t num_experts, const int32_t *offsets, const float *bias,
+                                      void *Y, int64_t ldy, q8_stream_t stream);
+
+enum { Q8_OP_LINEAR_W8A8 = 0, Q8_OP_LINEAR_INT8_MIXED = 1, Q8_OP_LINEAR_FP8_BLOCK = 2 };
 
 /* Bytes of device workspace an operation needs for these sizes (host function,
  * no device access).  The mixed operation sizes its outlier buffers for every
  * column being an outlier, so no call can overflow them.  Returns 0 for an
  * operation that needs none or for negative sizes, and SIZE_MAX when a size
- * exceeds 2^31 - 1 (no such call is valid). */
+ * exceeds what a call of that operation takes (2^31 - 1; 65535 * 128 for
+ * Q8_OP_LINEAR_FP8_BLOCK). */
 size_t q8_workspace_size(int op, int64_t m, int64_t n, int64_t k);
 
 /* Static, NUL-terminated description of a status code (host). */
