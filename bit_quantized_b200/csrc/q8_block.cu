@@ -384,7 +384,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                             // All of this warp's part is in registers: the buffer may be written again.
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(tempty0 + 8u * static_cast<uint32_t>(buf));
+                            if (lane == 0) mbar_arrive_cluster_no_fence(tempty0 + 8u * static_cast<uint32_t>(buf));
                         }
                         promote16(acc + c * 8, r[c & 1], s_cur[j]);
                     }
@@ -671,14 +671,18 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             buf ^= 1;
             if (buf == 0) bphase ^= 1;
         }
-        const uint32_t red_base = smem_addr(red);
+        // Token t goes to rank t % splits, slot [rank][t / splits][channel].
+        const uint32_t dst = smem_addr(red) + (rank * tpo * kBM + ch) * 4u;
+        uint32_t owner = 0, off = 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t < mt) {
-                const float v = (t & 1) ? acc[t / 2].y : acc[t / 2].x;
-                const uint32_t off = ((rank * tpo + t / splits) * kBM + ch) * 4u;
-                st_shared_cluster_u32(map_shared_rank(red_base + off, static_cast<uint32_t>(t % splits)),
-                                      __float_as_uint(v));
+                st_shared_cluster_u32(map_shared_rank(dst + off, owner),
+                                      __float_as_uint((t & 1) ? acc[t / 2].y : acc[t / 2].x));
+                if (++owner == static_cast<uint32_t>(splits)) {
+                    owner = 0;
+                    off += kBM * 4u;
+                }
             }
         }
         __syncwarp();
@@ -743,9 +747,10 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         if constexpr (QX) pdl_wait();   // Y may still be read by the previous kernel
         if (n < p.n && !abort_sh) {
             const float bias = p.bias ? p.bias[n] : 0.f;
-            for (int t = static_cast<int>(rank); t < mt; t += splits) {
+            const float* src = red + ch;
+            for (int t = static_cast<int>(rank); t < mt; t += splits, src += kBM) {
                 float s = 0.f;
-                for (int r = 0; r < splits; ++r) s = __fadd_rn(s, red[(r * tpo + t / splits) * kBM + ch]);
+                for (int r = 0; r < splits; ++r) s = __fadd_rn(s, src[r * tpo * kBM]);
                 if (p.bias) s = __fadd_rn(s, bias);
                 p.y[static_cast<int64_t>(t0 + t) * p.ldy + n] = __float2bfloat16_rn(s);
             }
