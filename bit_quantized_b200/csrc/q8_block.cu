@@ -470,25 +470,34 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
 // ============================================================================
 //
 // 128 output channels and up to NT tokens per cluster; the CTAs of a cluster
-// share the K groups and push their fp32 sums to the rank that finishes a
-// token, which adds them in rank order.  With QX the activation arrives
-// unquantized and four more warps quantize each group on its way into the stage (the
-// codes are those of the activation quantizer); without, TMA loads codes.
-//   warp 0 TMA, warp 1 MMA, warps 2-5 promotion and epilogue, warps 6-9 X.
+// share the K groups and push their fp32 sums, four tokens of a channel at a
+// time, to the rank that finishes those tokens, which adds them in rank order.
+// One warp runs these few-token phases at an instruction every nine cycles or
+// so, so from 32 tokens on two sets of four warps take half the columns each.
+// With QX the activation arrives unquantized and eight more warps quantize it
+// on its way into the stages (the codes are those of the activation
+// quantizer): a warp takes four tokens of one K group, and the groups go
+// round the warps, since one such piece is a chain of about 1000 cycles.
+//   warp 0 TMA, warp 1 MMA, then 4 or 8 promotion warps, then the quantizing ones.
+
+constexpr int kQxWarps = 8;
 
 template <int NT, bool QX>
 struct BlockDecodeCfg {
-    static constexpr int THREADS = QX ? 320 : 192;
+    static constexpr int HALVES = NT >= 32 ? 2 : 1;
+    static constexpr int PROMO = 4 * HALVES;
+    static constexpr int THREADS = 32 * (2 + PROMO + (QX ? kQxWarps : 0));
+    static constexpr int CW = NT / HALVES;       // columns per promotion warp
+    static constexpr int QUADS = NT / 4;
     static constexpr int A_BYTES = kBM * kBKB;   // 128 weight rows
     static constexpr int B_BYTES = NT * kBKB;    // NT token rows
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int RED_BYTES = (NT + 8) * kBM * 4;
-    static constexpr int STAGES_RAW = (227 * 1024 - 1024 - 8 * 1024 - RED_BYTES) / STAGE;
-    static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
-    // Scales of quantized-on-the-way groups: a stage is refilled when its MMA
+    static constexpr int MAX_STAGES = NT <= 64 ? 8 : 5;
+    // Scales of groups quantized on the way: a stage is refilled when its MMA
     // is done, with the promotion at most two groups behind the MMA.
-    static constexpr int SX_RING = STAGES + 2;
+    static constexpr int SX_RING = MAX_STAGES + 2;
     static constexpr int TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+    static_assert(!QX || NT == 16, "the quantizing warps cover 16 tokens");
 };
 
 template <int NT, bool QX, typename T>
@@ -499,39 +508,41 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     using C = BlockDecodeCfg<NT, QX>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    float* red = reinterpret_cast<float*>(smem + nstages * C::STAGE);   // [rank][tokens owned][128]
-    __shared__ __align__(8) uint64_t full_bar[C::STAGES];
-    __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+    float4* red = reinterpret_cast<float4*>(smem + nstages * C::STAGE);   // [rank][quads owned][128 channels]
+    __shared__ __align__(8) uint64_t full_bar[C::MAX_STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[C::MAX_STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2];
     __shared__ __align__(8) uint64_t tempty_bar[2];
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
-    __shared__ __align__(16) float col_s[4][NT];                   // promotion warps: Sx Sw of the group
+    __shared__ __align__(16) float col_s[C::PROMO][C::CW];         // promotion warps: Sx Sw of the group
     __shared__ float sx_ring[QX ? C::SX_RING : 1][QX ? NT : 1];
-    __shared__ __align__(8) uint64_t sx_bar[QX ? C::SX_RING : 1];  // four quantizing warps have written the slot
+    __shared__ __align__(8) uint64_t sx_bar[QX ? C::SX_RING : 1];  // every quad of the slot is written
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     const int tn = blockIdx.x;                       // 128 output channels
     const int t0 = static_cast<int>(blockIdx.z) * NT;
     const int mt = min(NT, p.m - t0);                // this tile's tokens
+    const int quads = (mt + 3) / 4;
     const uint32_t rank = cluster_ctarank();         // split index along K
     const int kb0 = static_cast<int>(rank) * kb_per_split;
     const int kb1 = min(num_kb, kb0 + kb_per_split);
     const int my_kb = kb1 > kb0 ? kb1 - kb0 : 0;
+    const int qpo = (quads + splits - 1) / splits;   // quads finished per rank
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < nstages; ++s) {
-            mbar_init(&full_bar[s], QX ? 5 : 1);     // TMA (and the four quantizing warps)
+            mbar_init(&full_bar[s], QX ? 1 + quads : 1);   // TMA (and the quantized quads)
             mbar_init(&empty_bar[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], 4);
+            mbar_init(&tempty_bar[b], C::PROMO);
         }
         if constexpr (QX)
-            for (int s = 0; s < C::SX_RING; ++s) mbar_init(&sx_bar[s], 4);
+            for (int s = 0; s < C::SX_RING; ++s) mbar_init(&sx_bar[s], quads);
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
         fence_barrier_init();
@@ -622,43 +633,52 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             }
         }
         __syncwarp();
-    } else if (warp < 6) {
-        const int q = warp & 3;
+    } else if (warp < 2 + C::PROMO) {
+        const int q = warp & 3, half = (warp - 2) / 4;
         const int ch = q * 32 + lane;
-        const int tpo = (NT + splits - 1) / splits;     // tokens owned per rank
+        const int c0 = half * C::CW;                    // this warp's first token column
+        const int cn = min(C::CW, mt - c0);             // and how many it has (may be none)
         const float* sw = p.sw + static_cast<int64_t>(tn) * num_kb;
-        float* cs = col_s[q];
-        float2 acc[NT / 2];
+        float* cs = col_s[warp - 2];
+        float2 acc[C::CW / 2];
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-        if constexpr (!QX) pdl_wait();
+        for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+        constexpr int NS = (C::CW + 31) / 32;           // column scales per lane
+        float sxv[NS], swk = my_kb > 0 ? __ldg(sw + kb0) : 0.f;
+        auto fetch_sx = [&](int kb) {
+#pragma unroll
+            for (int c = 0; c < NS; ++c) {
+                const int t = c * 32 + lane;
+                sxv[c] = t < cn ? __ldg(p.sx + static_cast<int64_t>(kb) * p.m + t0 + c0 + t) : 0.f;
+            }
+        };
+        if constexpr (!QX) {
+            pdl_wait();
+            if (my_kb > 0) fetch_sx(kb0);
+        }
         int buf = 0;
         uint32_t bphase = 0;
         for (int i = 0; i < my_kb; ++i) {
             const int kb = kb0 + i;
-            const float swk = __ldg(sw + kb);
-            if constexpr (!QX) {
-#pragma unroll
-                for (int c = 0; c < NT; c += 32) {
-                    const int t = c + lane;
-                    if (t < NT) cs[t] = t < mt ? p.sx[static_cast<int64_t>(kb) * p.m + t0 + t] * swk : 0.f;
-                }
-            }
             if constexpr (QX) {
                 if (!mbar_wait(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
+                if (lane < C::CW) cs[lane] = lane < cn ? sx_ring[i % C::SX_RING][lane] * swk : 0.f;
+            } else {
 #pragma unroll
-                for (int c = 0; c < NT; c += 32) {
-                    const int t = c + lane;
-                    if (t < NT) cs[t] = t < mt ? sx_ring[i % C::SX_RING][t] * swk : 0.f;
+                for (int c = 0; c < NS; ++c) {
+                    const int t = c * 32 + lane;
+                    if (t < C::CW) cs[t] = sxv[c] * swk;
                 }
+                if (i + 1 < my_kb) fetch_sx(kb + 1);
             }
+            if (i + 1 < my_kb) swk = __ldg(sw + kb + 1);
             if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
             __syncwarp();
             tc_fence_after();
-            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + c0;
 #pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-                if (c * 16 < mt) {
+            for (int c = 0; c < C::CW / 16; ++c) {
+                if (c * 16 < cn) {
                     uint32_t r[16];
                     tmem_ld16(tb + c * 16, r);
                     tmem_ld_wait();
@@ -671,65 +691,55 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             buf ^= 1;
             if (buf == 0) bphase ^= 1;
         }
-        // Token t goes to rank t % splits, slot [rank][t / splits][channel].
-        const uint32_t dst = smem_addr(red) + (rank * tpo * kBM + ch) * 4u;
-        uint32_t owner = 0, off = 0;
+        // Quad g of the tile goes to rank g % splits, slot [rank][g / splits][channel].
+        const uint32_t dst = smem_addr(red) + (rank * qpo * kBM + ch) * 16u;
+        uint32_t owner = static_cast<uint32_t>(c0 / 4 % splits), off = static_cast<uint32_t>(c0 / 4 / splits) * (kBM * 16u);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (t < mt) {
-                st_shared_cluster_u32(map_shared_rank(dst + off, owner),
-                                      __float_as_uint((t & 1) ? acc[t / 2].y : acc[t / 2].x));
+        for (int g = 0; g < C::CW / 4; ++g) {
+            if (g * 4 < cn) {
+                st_shared_cluster_v4(map_shared_rank(dst + off, owner),
+                                     make_float4(acc[2 * g].x, acc[2 * g].y, acc[2 * g + 1].x, acc[2 * g + 1].y));
                 if (++owner == static_cast<uint32_t>(splits)) {
                     owner = 0;
-                    off += kBM * 4u;
+                    off += kBM * 16u;
                 }
             }
         }
         __syncwarp();
     } else if constexpr (QX) {
-        // Quantizing warps: 8 lanes per token, 16 tokens per pass of the four warps.
+        // Piece (group i, quad): 8 lanes per token, 16 values each.
         pdl_wait();
-        const int qw = warp - 6;
-        const int sub = lane & 7;                       // 16-value piece of the group
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int i = 0; i < my_kb; ++i) {
-            const int kb = kb0 + i;
-            Eight<T> lo[NT / 16], hi[NT / 16];
-            const int col = kb * kBlock + sub * 16;
-#pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-                const int t = c * 16 + qw * 4 + lane / 8;
-                lo[c].zero();
-                hi[c].zero();
-                if (t < mt && col < k) {
-                    const T* src = X + static_cast<int64_t>(t0 + t) * ldx + col;
-                    lo[c].load(src);
-                    hi[c].load(src + 8);
-                }
+        const int qw = warp - 2 - C::PROMO;
+        const int sub = lane & 7, tl = lane / 8;
+        const int pieces = my_kb * quads;
+        auto load = [&](int piece, Eight<T>& lo, Eight<T>& hi) {
+            const int t = piece % quads * 4 + tl;
+            const int col = (kb0 + piece / quads) * kBlock + sub * 16;
+            lo.zero();
+            hi.zero();
+            if (t < mt && col < k) {
+                const T* src = X + static_cast<int64_t>(t0 + t) * ldx + col;
+                lo.load(src);
+                hi.load(src + 8);
             }
-            if (i >= nstages && !mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) break;
+        };
+        Eight<T> lo, hi;
+        if (qw < pieces) load(qw, lo, hi);
+        for (int piece = qw; piece < pieces; piece += kQxWarps) {
+            const int i = piece / quads, t = piece % quads * 4 + tl;
+            float s;
+            const uint4 w = quantize16<T>(lo, hi, s);
+            if (piece + kQxWarps < pieces) load(piece + kQxWarps, lo, hi);
+            const int stage = i % nstages, use = i / nstages;
+            if (use > 0 && !mbar_wait(&empty_bar[stage], (use - 1) & 1, &abort_sh, p.status)) break;
             __syncwarp();
-            uint8_t* sb = smem + stage * C::STAGE + C::A_BYTES;
-#pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-                const int t = c * 16 + qw * 4 + lane / 8;
-                if (c * 16 < mt) {                      // uniform over the warp
-                    float s;
-                    const uint4 w = quantize16<T>(lo[c], hi[c], s);
-                    st_shared_v4(sb + t * kBKB + ((sub ^ (t & 7)) << 4), w.x, w.y, w.z, w.w);
-                    if (sub == 0) sx_ring[i % C::SX_RING][t] = s;
-                }
-            }
+            st_shared_v4(smem + stage * C::STAGE + C::A_BYTES + t * kBKB + ((sub ^ (t & 7)) << 4), w.x, w.y, w.z, w.w);
+            if (sub == 0) sx_ring[i % C::SX_RING][t] = s;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&full_bar[stage]);
                 mbar_arrive(&sx_bar[i % C::SX_RING]);
-            }
-            if (++stage == nstages) {
-                stage = 0;
-                phase ^= 1;
             }
         }
         __syncwarp();
@@ -740,19 +750,26 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     __syncthreads();
     cluster_sync();
 
-    if (warp >= 2 && warp < 6) {
-        const int ch = (warp & 3) * 32 + lane;
-        const int tpo = (NT + splits - 1) / splits;
+    if (warp >= 2 && warp < 2 + C::PROMO) {
+        const int ch = (warp & 3) * 32 + lane, half = (warp - 2) / 4;
         const int n = tn * kBM + ch;
         if constexpr (QX) pdl_wait();   // Y may still be read by the previous kernel
         if (n < p.n && !abort_sh) {
             const float bias = p.bias ? p.bias[n] : 0.f;
-            const float* src = red + ch;
-            for (int t = static_cast<int>(rank); t < mt; t += splits, src += kBM) {
-                float s = 0.f;
-                for (int r = 0; r < splits; ++r) s = __fadd_rn(s, src[r * tpo * kBM]);
-                if (p.bias) s = __fadd_rn(s, bias);
-                p.y[static_cast<int64_t>(t0 + t) * p.ldy + n] = __float2bfloat16_rn(s);
+            for (int sl = half, g = static_cast<int>(rank) + half * splits; g < quads; sl += C::HALVES, g += C::HALVES * splits) {
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int r = 0; r < splits; ++r) {
+                    const float4 v = red[(r * qpo + sl) * kBM + ch];
+                    s.x = __fadd_rn(s.x, v.x);
+                    s.y = __fadd_rn(s.y, v.y);
+                    s.z = __fadd_rn(s.z, v.z);
+                    s.w = __fadd_rn(s.w, v.w);
+                }
+                const float o[4] = {s.x, s.y, s.z, s.w};
+                __nv_bfloat16* y = p.y + static_cast<int64_t>(t0 + 4 * g) * p.ldy + n;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * g + e < mt) y[e * p.ldy] = __float2bfloat16_rn(p.bias ? __fadd_rn(o[e], bias) : o[e]);
             }
         }
     }
@@ -857,16 +874,23 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
     const int tiles_t = static_cast<int>((a.m + NT - 1) / NT);
     const int num_kb = static_cast<int>((a.k + kBKB - 1) / kBKB);
     // Split K across the CTAs of a cluster (at most 8, every split non-empty)
-    // so that the grid fills the SMs at two CTAs per SM, which the short stage
-    // ring of a split allows.
-    int want = 2 * sm_count() / (tiles_n * tiles_t);
+    // as far as one wave holds: two CTAs per SM up to 32 tokens (a short stage
+    // ring), else one, and about 128 SMs where clusters of four and eight fit.
+    const int per_sm = NT <= 32 ? 2 : 1;
+    int want = 128 * per_sm / (tiles_n * tiles_t);
     if (want < 1) want = 1;
     if (want > 8) want = 8;
     if (want > num_kb) want = num_kb;
     const int per = (num_kb + want - 1) / want;
     const int splits = (num_kb + per - 1) / per;
-    const int nstages = per < C::STAGES ? per : C::STAGES;
-    const int smem = nstages * C::STAGE + C::RED_BYTES + 1024;
+    const int quads = ((a.m < NT ? static_cast<int>(a.m) : NT) + 3) / 4;
+    const int red = splits * ((quads + splits - 1) / splits) * kBM * 16;
+    const int budget = (tiles_n * tiles_t * splits > sm_count() ? 113 : 220) * 1024 - 4 * 1024 - red;
+    int nstages = budget / C::STAGE;
+    if (nstages > C::MAX_STAGES) nstages = C::MAX_STAGES;
+    if (nstages > per) nstages = per;
+    if (nstages < 1) nstages = 1;
+    const int smem = nstages * C::STAGE + red + 1024;
     if (set_smem(kern, smem) != cudaSuccess) return Q8_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles_n), static_cast<unsigned>(splits), static_cast<unsigned>(tiles_t));
@@ -888,13 +912,6 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
         return Q8_ERR_LAUNCH;
     }
     return Q8_OK;
-}
-
-template <typename T>
-q8_status run_fused(const BlockLinearArgs& a, cudaStream_t s) {
-    if (a.m <= 16) return run_block_decode<16, true, T>(a, s);
-    if (a.m <= 32) return run_block_decode<32, true, T>(a, s);
-    return run_block_decode<64, true, T>(a, s);
 }
 
 // Tile width of the pair kernel: the persistent grid's makespan, waves x (BN +
@@ -925,9 +942,9 @@ q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     }
     if (a.x) {   // quantized on the way
         switch (a.x_dtype) {
-            case Q8_F16: return run_fused<__half>(a, s);
-            case Q8_BF16: return run_fused<__nv_bfloat16>(a, s);
-            default: return run_fused<float>(a, s);
+            case Q8_F16: return run_block_decode<16, true, __half>(a, s);
+            case Q8_BF16: return run_block_decode<16, true, __nv_bfloat16>(a, s);
+            default: return run_block_decode<16, true, float>(a, s);
         }
     }
     if (a.m <= 16) return run_block_decode<16, false, __half>(a, s);

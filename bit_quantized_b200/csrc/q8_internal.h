@@ -150,7 +150,7 @@ struct BlockLinearArgs {
 };
 
 // Tokens up to which a dynamic call quantizes inside the GEMM.
-constexpr int64_t kBlockFusedTokens = 64;
+constexpr int64_t kBlockFusedTokens = 16;
 
 q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s);
 

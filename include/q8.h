@@ -555,12 +555,12 @@ q8_status q8_quantize_weight_block(const void *W, q8_dtype w_dtype, int64_t expe
  *   bias    device [n] fp32, or NULL.
  *   Y       device, m x n bf16, row stride ldy >= n, ldy % 8 == 0.
  * The dynamic form takes the unquantized activation and gives the result of
- * q8_quantize_act_block followed by q8_linear_fp8_block; up to 64 tokens it
+ * q8_quantize_act_block followed by q8_linear_fp8_block; up to 16 tokens it
  * quantizes inside the GEMM (one launch, no workspace), above that into the
  * workspace (two launches).
  *   X          device, Q8_F16, Q8_BF16 or Q8_F32, row stride ldx.
  *   workspace  at least q8_workspace_size(Q8_OP_LINEAR_FP8_BLOCK, m, n, k)
- *              bytes (0 up to 64 tokens), 256-byte aligned; needs no
+ *              bytes (0 up to 16 tokens), 256-byte aligned; needs no
  *              initialization.  Calls that overlap on the GPU need one each.
  * The launch-overlap rule of q8_linear_w8a8 applies to codes and scales of
  * the weight.
