@@ -110,6 +110,10 @@ q8_status check_weight_block(const q8_weight_block* w, int64_t experts) {
     return Q8_OK;
 }
 
+// Hidden and intermediate sizes of the expert layer: its steps (experts x
+// 128-wide tiles x K groups) are counted in 32 bits.
+constexpr int64_t kMaxMoeDim = 65536;
+
 // Output tiles of a block-scaled linear are counted in 32 bits.
 bool block_tiles_fit(int64_t m, int64_t n, int64_t experts) {
     return ((m + 255) / 256 + experts) * blocks128(n) <= kMaxDim;
@@ -777,6 +781,73 @@ q8_status q8_linear_fp8_block_grouped(const q8_act_block* x, const q8_weight_blo
     a.bias = bias;
     a.y = static_cast<__nv_bfloat16*>(Y); a.ldy = ldy;
     return launch_block_linear(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+q8_status q8_moe_route(const void* logits, q8_dtype dtype, int64_t m, int64_t num_experts, int64_t ld,
+                       int64_t top_k, q8_scoring scoring, int32_t renormalize, int32_t* ids, float* weights,
+                       q8_stream_t stream) {
+    if (m < 0 || m > kMaxDim || num_experts < 1 || num_experts > kMoeMaxExperts || top_k < 1 ||
+        top_k > kMoeMaxTopK || top_k > num_experts || ld < num_experts)
+        return Q8_ERR_SHAPE;
+    if (!float_input(dtype)) return Q8_ERR_DTYPE;
+    if (scoring != Q8_SOFTMAX && scoring != Q8_SIGMOID) return Q8_ERR_SCHEME;
+    if (m == 0) return Q8_OK;   // empty call
+    if (!logits || !ids || !weights) return Q8_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(logits) % static_cast<unsigned>(elem_bytes(dtype)) != 0 ||
+        (reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
+        return Q8_ERR_ALIGN;
+    q8_status st = check_device();
+    if (st != Q8_OK) return st;
+    MoeRouteArgs a = {};
+    a.logits = logits; a.dtype = dtype;
+    a.ld = ld; a.m = m; a.experts = num_experts; a.top_k = top_k;
+    a.sigmoid = scoring == Q8_SIGMOID; a.renormalize = renormalize != 0;
+    a.ids = ids; a.weights = weights;
+    return launch_status(launch_moe_route(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t q8_moe_workspace_size(int64_t m, int64_t top_k, int64_t num_experts, int64_t hidden, int64_t inter) {
+    if (m < 0 || top_k < 1 || num_experts < 1 || hidden < 0 || inter < 0) return 0;
+    if (m > kMoeMaxTokens || top_k > kMoeMaxTopK || num_experts > kMoeMaxExperts || hidden > kMaxMoeDim ||
+        inter > kMaxMoeDim)
+        return SIZE_MAX;
+    MoeLayerArgs a = {};
+    a.m = m; a.top_k = top_k; a.experts = num_experts; a.hidden = hidden; a.inter = inter;
+    return static_cast<size_t>(moe_workspace_bytes(a));
+}
+
+q8_status q8_moe_fp8_block(const void* X, q8_dtype x_dtype, int64_t m, int64_t hidden, int64_t ldx,
+                           const int32_t* ids, const float* weights, int64_t top_k,
+                           const q8_weight_block* w13, const q8_weight_block* w2, int64_t num_experts, void* Y,
+                           int64_t ldy, void* workspace, size_t ws_bytes, q8_stream_t stream) {
+    if (!w13 || !w2) return Q8_ERR_NULL;
+    if (num_experts < 1 || num_experts > kMoeMaxExperts) return Q8_ERR_SHAPE;
+    q8_status st = check_weight_block(w13, num_experts);
+    if (st == Q8_OK) st = check_weight_block(w2, num_experts);
+    if (st != Q8_OK) return st;
+    const int64_t inter = w2->k;
+    if (m < 0 || m > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || hidden > kMaxMoeDim ||
+        inter > kMaxMoeDim || inter % 128 != 0 || w13->k != hidden || w13->n != num_experts * 2 * inter ||
+        w2->n != num_experts * hidden || ldx < hidden || ldy < hidden)
+        return Q8_ERR_SHAPE;
+    if (!float_input(x_dtype)) return Q8_ERR_DTYPE;
+    if (m == 0) return Q8_OK;   // empty call
+    if (!X || !ids || !weights || !Y) return Q8_ERR_NULL;
+    if (!aligned16(X) || !ld_ok(ldx, hidden, x_dtype) || !aligned16(Y) || ldy % 8 != 0 ||
+        (reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
+        return Q8_ERR_ALIGN;
+    if (!workspace || ws_bytes < q8_moe_workspace_size(m, top_k, num_experts, hidden, inter)) return Q8_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return Q8_ERR_ALIGN;
+    st = check_device();
+    if (st != Q8_OK) return st;
+    MoeLayerArgs a = {};
+    a.x = X; a.x_dtype = x_dtype;
+    a.m = m; a.hidden = hidden; a.ldx = ldx; a.top_k = top_k; a.experts = num_experts; a.inter = inter;
+    a.ids = ids; a.weights = weights;
+    a.w13 = w13->codes; a.ld13 = w13->ld; a.s13 = w13->scale;
+    a.w2 = w2->codes; a.ld2 = w2->ld; a.s2 = w2->scale;
+    a.y = static_cast<__nv_bfloat16*>(Y); a.ldy = ldy;
+    return launch_moe_layer(a, static_cast<uint8_t*>(workspace), reinterpret_cast<cudaStream_t>(stream));
 }
 
 q8_status q8_get_device_status(int32_t* out, q8_stream_t stream) {

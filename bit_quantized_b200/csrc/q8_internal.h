@@ -154,4 +154,29 @@ constexpr int64_t kBlockFusedTokens = 16;
 
 q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s);
 
+// ---- expert layer for a few tokens (q8_moe_block.cu)
+constexpr int64_t kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 512;
+constexpr int64_t kMoeMaxCtas = 160;       // CTAs of a projection (the workspace has room for their sums)
+
+struct MoeRouteArgs {
+    const void* logits; q8_dtype dtype;    // m x experts, row stride ld
+    int64_t ld, m, experts, top_k;
+    bool sigmoid, renormalize;
+    int32_t* ids; float* weights;          // m x top_k
+};
+
+cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t s);
+
+struct MoeLayerArgs {
+    const void* x; q8_dtype x_dtype;       // m x hidden, row stride ldx
+    int64_t m, hidden, ldx, top_k, experts, inter;
+    const int32_t* ids; const float* weights;   // m x top_k
+    const void* w13; int64_t ld13; const float* s13;   // experts * 2 inter x hidden
+    const void* w2; int64_t ld2; const float* s2;      // experts * hidden x inter
+    __nv_bfloat16* y; int64_t ldy;
+};
+
+int64_t moe_workspace_bytes(const MoeLayerArgs& a);   // from m, top_k, experts, hidden and inter
+q8_status launch_moe_layer(const MoeLayerArgs& a, uint8_t* workspace, cudaStream_t s);
+
 }  // namespace q8

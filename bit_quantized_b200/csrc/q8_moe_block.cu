@@ -1,0 +1,953 @@
+// The expert layer of a mixture of experts for a few tokens, on block-scaled
+// FP8 weights, and the router's choice.
+//
+//   route   the top_k largest logits of a token (the lowest index first among
+//           equals), weighted by a softmax or a sigmoid
+//   layer   G, U = W13[e] q(x_t),  h = q(silu(G) * U),
+//           y_t = sum over the token's experts e of w[t, e] W2[e] h
+//           with q the quantizer of one scale per token and 128 values
+//
+// For a few tokens the layer is the stream of the chosen experts' weights, so
+// both projections divide that stream evenly: the K groups of all active
+// experts' 128-channel tiles form one line of steps, and every CTA takes an
+// equal, contiguous piece of it (weights on the MMA's M side, tokens as N).
+// Where a piece ends inside a tile, the fp32 sums go to the workspace, and the
+// CTA that arrives last adds them in the order of the CTAs, so results repeat
+// bit for bit.  Three launches:
+//   moe_prepare_kernel  quantizes x once, lists the active experts with their
+//                       tokens, and clears the arrival counters;
+//   moe_up_kernel       gate and up tiles side by side, SwiGLU and the
+//                       quantization of h in the epilogue (a tile is 128 wide:
+//                       one scale group of h);
+//   moe_down_kernel     goes through the experts of an output tile one after
+//                       the other, so the weighted sum over experts stays in
+//                       the CTA's shared memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "q8_block.cuh"
+#include "q8_internal.h"
+#include "q8_tile.cuh"
+
+namespace q8 {
+namespace {
+
+constexpr int kBM = 128;
+constexpr int kBKB = 128;
+constexpr int kMaxTokens = kMoeMaxTokens;
+constexpr int kMaxExperts = kMoeMaxExperts;
+constexpr int kMinSteps = 4;   // fewest K groups worth a CTA of its own
+
+// ============================================================================
+// Router
+// ============================================================================
+//
+// One warp per token, 16 logits per lane.  A logit becomes an ordered 32-bit
+// key (0: not to be chosen), so a round of the selection is one warp maximum
+// and, for the lowest index among equals, one warp minimum.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (!(v > -INFINITY)) return 0u;                   // -inf and NaN are never chosen
+    v = fminf(v, FLT_MAX) + 0.0f;                      // -0 equals 0
+    const uint32_t b = __float_as_uint(v);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__global__ void __launch_bounds__(128)
+moe_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t m, int experts, int top_k, int sigmoid,
+                 int renormalize, int32_t* __restrict__ ids, float* __restrict__ weights) {
+    const int lane = threadIdx.x % 32;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (t >= m) return;
+    constexpr int V = kMaxExperts / 32;
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < experts ? order_key(to_float(logits[t * ld + e])) : 0u;
+    }
+    uint32_t lead = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) lead = max(lead, key[i]);
+    lead = __reduce_max_sync(0xffffffffu, lead);
+    const float top = lead ? key_value(lead) : 0.f;
+    float total = 0.f;
+    if (!sigmoid && !renormalize) {                    // softmax over all experts
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i]) total += expf(key_value(key[i]) - top);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    int my_id = -1;                                    // lane s: slot s
+    float my_w = 0.f;
+    for (int s = 0; s < top_k; ++s) {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (best == 0u) break;
+        uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (key[i] == best) at = static_cast<uint32_t>(i * 32 + lane);
+        at = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (static_cast<uint32_t>(i * 32 + lane) == at) key[i] = 0u;
+        if (lane == s) {
+            my_id = static_cast<int>(at);
+            const float v = key_value(best);
+            my_w = sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top);
+        }
+    }
+    if (renormalize) {
+        total = my_w;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane < top_k) {
+        if (renormalize || !sigmoid) my_w = total > 0.f ? my_w / total : 0.f;
+        ids[t * top_k + lane] = my_id;
+        weights[t * top_k + lane] = my_w;
+    }
+}
+
+// ============================================================================
+// Preparation: x in 8 bits, the active experts, cleared counters
+// ============================================================================
+
+struct MoeParams {
+    int m, top_k, experts, hidden, inter;
+    int rows_max;            // m * top_k
+    int it, ht, kb1, kb2;    // 128-wide tiles of inter and hidden; K groups of both products (kb1 = ht, kb2 = it)
+    int* head;               // [0] active experts, [1] rows
+    int* expert; int* base;
+    unsigned long long* mask;
+    int* row_token; float* row_weight;
+    int* up_count; int* down_count;
+    uint8_t* xq; float* xs;  // m x hidden codes, [kb1][m]
+    uint8_t* hq; float* hs;  // rows x inter codes, [kb2][rows_max]
+    float* part;             // sums of unfinished tiles
+    const float* s13; const float* s2;
+    __nv_bfloat16* y; int64_t ldy;
+    int* status;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restrict__ ids,
+                   const float* __restrict__ weights, const MoeParams p) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (blockIdx.x + 1 < gridDim.x) {
+        // 256 columns (two groups) of every token; a warp takes a token at a time.
+        const int col = static_cast<int>(blockIdx.x) * 256 + lane * 8;
+        pdl_wait();
+        pdl_launch_dependents();
+        for (int t = warp; t < p.m; t += 8) {
+            Eight<T> v;
+            if (col < p.hidden) v.load(X + static_cast<int64_t>(t) * ldx + col);
+            else v.zero();
+            float f[8];
+            v.values(f);
+            float a = absmax8(f);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const BlockScale s = block_scale(a);
+            if (col < p.hidden) {
+                *reinterpret_cast<uint2*>(p.xq + static_cast<int64_t>(t) * p.hidden + col) =
+                    make_uint2(block_codes4(f[0], f[1], f[2], f[3], s), block_codes4(f[4], f[5], f[6], f[7], s));
+                if (lane % 16 == 0) p.xs[static_cast<int64_t>(col / kBlock) * p.m + t] = s.S;
+            }
+        }
+        return;
+    }
+    // The last block: tokens of every expert as a bit mask (an expert that a
+    // token names twice has it once, with both weights), then the list.
+    __shared__ unsigned long long mask_sh[kMaxExperts];
+    __shared__ int list_sh[kMaxExperts], base_sh[kMaxExperts];
+    __shared__ int active_sh, rows_sh;
+    for (int e = threadIdx.x; e < p.experts; e += 256) mask_sh[e] = 0ull;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = threadIdx.x; i < p.rows_max; i += 256) {
+        const int e = ids[i];
+        if (e >= 0 && e < p.experts) atomicOr(&mask_sh[e], 1ull << (i / p.top_k));
+    }
+    for (int i = threadIdx.x; i < min(p.experts, p.rows_max) * p.it; i += 256) p.up_count[i] = 0;
+    for (int i = threadIdx.x; i < p.ht; i += 256) p.down_count[i] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int na = 0, nr = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            const int e = e0 + lane;
+            const int c = e < p.experts ? __popcll(mask_sh[e]) : 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, c > 0);
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (c > 0) {
+                const int a = na + __popc(some & ((1u << lane) - 1u));
+                list_sh[a] = e;
+                base_sh[a] = nr + incl - c;
+            }
+            na += __popc(some);
+            nr += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            active_sh = na;
+            rows_sh = nr;
+        }
+    }
+    __syncthreads();
+    const int na = active_sh;
+    if (threadIdx.x == 0) {
+        p.head[0] = na;
+        p.head[1] = rows_sh;
+    }
+    for (int a = threadIdx.x; a < na; a += 256) {
+        const int e = list_sh[a];
+        const unsigned long long mk = mask_sh[e];
+        p.expert[a] = e;
+        p.base[a] = base_sh[a];
+        p.mask[a] = mk;
+        int r = base_sh[a];
+        for (unsigned long long b = mk; b; b &= b - 1) {
+            const int t = __ffsll(static_cast<long long>(b)) - 1;
+            float w = 0.f;
+            for (int s = 0; s < p.top_k; ++s)
+                if (ids[t * p.top_k + s] == e) w += weights[t * p.top_k + s];
+            p.row_token[r] = t;
+            p.row_weight[r] = w;
+            ++r;
+        }
+    }
+}
+
+// ============================================================================
+// The two products
+// ============================================================================
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A CTA's piece of the line of steps, and which CTA a step belongs to.
+struct Line {
+    long long total;
+    int ctas;
+    __device__ __forceinline__ Line(long long t) : total(t) {
+        long long c = t / kMinSteps;
+        ctas = static_cast<int>(c < 1 ? 1 : (c < static_cast<long long>(gridDim.x) ? c : static_cast<long long>(gridDim.x)));
+    }
+    __device__ __forceinline__ int start(int c) const { return static_cast<int>(total * c / ctas); }
+    __device__ __forceinline__ int owner(int s) const {
+        return static_cast<int>(((static_cast<long long>(s) + 1) * ctas - 1) / total);
+    }
+};
+
+// Counts this CTA's arrival at a tile with `parts` contributors; true in the
+// one that arrives last, which then sees every contributor's sums.  Called by
+// the `threads` threads of the promotion warps, after each wrote its sums.
+__device__ __forceinline__ bool arrive_last(int* counter, int parts, int* flag_sh, bool leader, int barrier, int threads) {
+    __threadfence();
+    named_barrier(barrier, threads);
+    if (leader) {
+        *flag_sh = atomicAdd(counter, 1) == parts - 1;
+        __threadfence();
+    }
+    named_barrier(barrier, threads);
+    const bool last = *flag_sh != 0;
+    named_barrier(barrier, threads);   // the flag may be written again
+    return last;
+}
+
+template <int NT>
+struct MoeUpCfg {
+    static constexpr int HALVES = NT >= 32 ? 2 : 1;
+    static constexpr int PROMO = 4 * HALVES;
+    static constexpr int THREADS = 32 * (2 + PROMO);
+    static constexpr int CW = NT / HALVES;            // token columns per promotion warp
+    static constexpr int B_BYTES = NT * kBKB;
+    static constexpr int STAGE = 2 * kBM * kBKB + B_BYTES;
+    static constexpr int STAGES = (200 * 1024) / STAGE;
+    static constexpr int TMEM_COLS = 4 * NT;
+    static constexpr int SMEM = STAGES * STAGE + 1024;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(MoeUpCfg<NT>::THREADS, 1)
+moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const MoeParams p) {
+    using C = MoeUpCfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2];
+    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh, last_sh;
+    __shared__ __align__(16) float col_s[C::PROMO][2][C::CW];
+    __shared__ float amax_sh[C::HALVES][4][C::CW];
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], C::PROMO);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_sh = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_base_sh;
+    pdl_wait();
+    // The down projection may start: it reads the expert list, which is
+    // complete here, before it waits for this kernel.
+    pdl_launch_dependents();
+
+    const int active = p.head[0];
+    const Line line(static_cast<long long>(active) * p.it * p.kb1);
+    const int cta = static_cast<int>(blockIdx.x);
+    const int s_begin = active > 0 && cta < line.ctas ? line.start(cta) : 0;
+    const int s_end = active > 0 && cta < line.ctas ? line.start(cta + 1) : 0;
+
+    if (warp == 0) {
+        if (elect_one() && s_begin < s_end) {
+            tma_prefetch_desc(&tmW);
+            tma_prefetch_desc(&tmX);
+            uint32_t issued = 0, last_par = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int s = s_begin; s < s_end && ok;) {
+                const int u = s / p.kb1, k0 = s - u * p.kb1;
+                const int k1 = min(p.kb1, k0 + s_end - s);
+                const int a = u / p.it;
+                const int row = p.expert[a] * 2 * p.inter + (u - a * p.it) * kBM;
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sa = smem + stage * C::STAGE;
+                    mbar_arrive_expect_tx(&full_bar[stage], C::STAGE);
+                    tma_load_2d(sa, &tmW, &full_bar[stage], kb * kBKB, row);
+                    tma_load_2d(sa + kBM * kBKB, &tmW, &full_bar[stage], kb * kBKB, row + p.inter);
+                    tma_load_2d(sa + 2 * kBM * kBKB, &tmX, &full_bar[stage], kb * kBKB, 0);
+                    issued |= 1u << stage;
+                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                s += k1 - k0;
+            }
+            if (!ok)   // the loads already issued land before the CTA leaves
+                for (int t = 0; t < C::STAGES; ++t)
+                    if (issued & (1u << t)) mbar_wait(&full_bar[t], (last_par >> t) & 1, nullptr, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((p.m + 15) / 16 * 16));
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int s = s_begin; s < s_end; ++s) {
+                if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                    !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_addr(smem + stage * C::STAGE);
+                const uint64_t gd = sdesc_kmajor_sw128(sa), ud = sdesc_kmajor_sw128(sa + kBM * kBKB);
+                const uint64_t bd = sdesc_kmajor_sw128(sa + 2 * kBM * kBKB);
+                const uint32_t d = tmem_base + buf * 2 * NT;
+#pragma unroll
+                for (int ks = 0; ks < kBKB / 32; ++ks) {
+                    mma_issue<kKindF8>(d, gd + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    mma_issue<kKindF8>(d + NT, ud + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                }
+                tc_commit(&tfull_bar[buf]);
+                tc_commit(&empty_bar[stage]);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1;
+            }
+            if (!ok) {
+                tc_commit(&drain_bar);
+                mbar_wait(&drain_bar, 0, nullptr, nullptr);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int q = warp & 3, half = (warp - 2) / 4;
+        const int ch = q * 32 + lane;
+        const int c0 = half * C::CW;
+        float* cs = &col_s[warp - 2][0][0];
+        int buf = 0;
+        uint32_t bphase = 0;
+        // After a wait that ran out, the warps stop waiting and reading TMEM but
+        // take the same barriers to the end (the status word tells the caller).
+        bool ok = true;
+        for (int s = s_begin; s < s_end;) {
+            const int u = s / p.kb1, k0 = s - u * p.kb1;
+            const int k1 = min(p.kb1, k0 + s_end - s);
+            const int a = u / p.it, it = u - a * p.it;
+            const int e = p.expert[a];
+            // this warp's columns that the expert's tokens fill
+            const uint32_t want = static_cast<uint32_t>((p.mask[a] >> c0) & ((1ull << C::CW) - 1ull));
+            const float* sg = p.s13 + (static_cast<int64_t>(e) * 2 * p.it + it) * p.kb1;
+            const float* su = sg + static_cast<int64_t>(p.it) * p.kb1;
+            float2 g[C::CW / 2], w[C::CW / 2];
+#pragma unroll
+            for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
+            const int t = c0 + lane;                        // CW <= 32: one column scale per lane
+            const bool have = lane < C::CW && t < p.m;
+            float sx = have ? __ldcg(p.xs + static_cast<int64_t>(k0) * p.m + t) : 0.f;
+            float wg = __ldg(sg + k0), wu = __ldg(su + k0);
+            for (int kb = k0; kb < k1; ++kb) {
+                __syncwarp();
+                if (lane < C::CW) {
+                    cs[lane] = sx * wg;
+                    cs[C::CW + lane] = sx * wu;
+                }
+                if (kb + 1 < k1) {
+                    sx = have ? __ldcg(p.xs + static_cast<int64_t>(kb + 1) * p.m + t) : 0.f;
+                    wg = __ldg(sg + kb + 1);
+                    wu = __ldg(su + kb + 1);
+                }
+                ok = ok && mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 2 * NT + c0;
+#pragma unroll
+                for (int c = 0; c < C::CW / 16; ++c) {
+                    if ((want >> (c * 16)) & 0xFFFFu) {
+                        uint32_t rg[16], ru[16];
+                        tmem_ld16(tb + c * 16, rg);
+                        tmem_ld16(tb + NT + c * 16, ru);
+                        tmem_ld_wait();
+                        promote16(g + c * 8, rg, cs + c * 16);
+                        promote16(w + c * 8, ru, cs + C::CW + c * 16);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1;
+            }
+            bool finish = true;
+            if (k1 - k0 < p.kb1) {
+                // A piece of a tile: [cta][first or last tile][gate, up][column][channel].
+                float* mine = p.part + (static_cast<int64_t>(cta) * 2 + (k0 > 0 ? 0 : 1)) * (2 * NT * kBM) + ch;
+#pragma unroll
+                for (int i = 0; i < C::CW; ++i) {
+                    if ((want >> i) & 1u) {
+                        mine[(c0 + i) * kBM] = (i & 1) ? g[i / 2].y : g[i / 2].x;
+                        mine[(NT + c0 + i) * kBM] = (i & 1) ? w[i / 2].y : w[i / 2].x;
+                    }
+                }
+                const int first = line.owner(u * p.kb1), lastc = line.owner((u + 1) * p.kb1 - 1);
+                finish = arrive_last(&p.up_count[u], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1, 32 * C::PROMO);
+                if (finish) {
+#pragma unroll
+                    for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
+                    for (int c = first; c <= lastc; ++c) {
+                        const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
+#pragma unroll
+                        for (int i = 0; i < C::CW; ++i) {
+                            if ((want >> i) & 1u) {
+                                const float x = __ldcg(src + (c0 + i) * kBM), v = __ldcg(src + (NT + c0 + i) * kBM);
+                                if (i & 1) {
+                                    g[i / 2].y += x;
+                                    w[i / 2].y += v;
+                                } else {
+                                    g[i / 2].x += x;
+                                    w[i / 2].x += v;
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            if (finish) {
+                // h = silu(G) U of this tile: one scale group of h per token.
+                const int rbase = p.base[a] + __popcll(p.mask[a] & ((1ull << c0) - 1ull));
+#pragma unroll
+                for (int i = 0; i < C::CW; ++i) {
+                    if ((want >> i) & 1u) {
+                        float& gi = (i & 1) ? g[i / 2].y : g[i / 2].x;
+                        const float ui = (i & 1) ? w[i / 2].y : w[i / 2].x;
+                        gi = gi / (1.0f + expf(-gi)) * ui;
+                        const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(gi)));
+                        if (lane == 0) amax_sh[half][q][i] = __uint_as_float(am);
+                    }
+                }
+                named_barrier(2 + half, 128);
+#pragma unroll
+                for (int i = 0; i < C::CW; ++i) {
+                    if ((want >> i) & 1u) {
+                        const int r = rbase + __popc(want & ((1u << i) - 1u));
+                        const float am = fmaxf(fmaxf(amax_sh[half][0][i], amax_sh[half][1][i]),
+                                               fmaxf(amax_sh[half][2][i], amax_sh[half][3][i]));
+                        const BlockScale bs = block_scale(am);
+                        const float hi = (i & 1) ? g[i / 2].y : g[i / 2].x;
+                        p.hq[static_cast<int64_t>(r) * p.inter + it * kBM + ch] =
+                            static_cast<uint8_t>(block_codes4(hi, 0.f, 0.f, 0.f, bs) & 0xFFu);
+                        if (ch == 0) p.hs[static_cast<int64_t>(it) * p.rows_max + r] = bs.S;
+                    }
+                }
+                named_barrier(2 + half, 128);   // amax_sh may be written again
+            }
+            s += k1 - k0;
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+template <int NT>
+struct MoeDownCfg {
+    static constexpr int THREADS = 192;
+    static constexpr int B_BYTES = NT * kBKB;
+    static constexpr int STAGE = kBM * kBKB + B_BYTES;
+    static constexpr int OUT = NT * kBM * 4;          // the tile's sums over experts
+    static constexpr int STAGES_RAW = (200 * 1024 - OUT) / STAGE;
+    static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
+    static constexpr int TMEM_COLS = 2 * NT;
+    static constexpr int SMEM = STAGES * STAGE + OUT + 1024;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(MoeDownCfg<NT>::THREADS, 1)
+moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const MoeParams p) {
+    using C = MoeDownCfg<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    float* out = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);   // [token][channel]
+    __shared__ __align__(8) uint64_t full_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+    __shared__ __align__(8) uint64_t tfull_bar[2];
+    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t drain_bar;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh, last_sh;
+    __shared__ __align__(16) float col_s[4][NT];
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full_bar[s], 1);
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull_bar[b], 1);
+            mbar_init(&tempty_bar[b], 4);
+        }
+        mbar_init(&drain_bar, 1);
+        abort_sh = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tmem_base_sh;
+    pdl_launch_dependents();
+
+    // The expert list was complete before the up projection let this kernel start.
+    const int active = __ldcg(p.head);
+    const int tile_steps = active * p.kb2;           // of one output tile
+    const Line line(static_cast<long long>(tile_steps) * p.ht);
+    const int cta = static_cast<int>(blockIdx.x);
+    const int s_begin = active > 0 && cta < line.ctas ? line.start(cta) : 0;
+    const int s_end = active > 0 && cta < line.ctas ? line.start(cta + 1) : 0;
+
+    if (warp == 0) {
+        if (elect_one() && s_begin < s_end) {
+            tma_prefetch_desc(&tmW);
+            tma_prefetch_desc(&tmH);
+            uint32_t issued = 0, last_par = 0;
+            bool ok = true;
+            // Pass 0 asks for the first ring's weights, before the up
+            // projection is done; pass 1 for everything else.
+            const int first = min(s_end - s_begin, C::STAGES);
+            for (int pass = 0; pass < 2 && ok; ++pass) {
+                if (pass == 1) pdl_wait();
+                int stage = 0;
+                uint32_t phase = 0;
+                const int end = pass == 0 ? s_begin + first : s_end;
+                for (int s = s_begin; s < end && ok;) {
+                    const int v = s / p.kb2, k0 = s - v * p.kb2;
+                    const int k1 = min(p.kb2, k0 + end - s);
+                    const int nt = v / active, a = v - nt * active;
+                    const int row = __ldcg(p.expert + a) * p.hidden + nt * kBM;
+                    const int base = __ldcg(p.base + a);
+                    const int boxes = (__popcll(__ldcg(p.mask + a)) + 15) / 16;
+                    for (int kb = k0; kb < k1; ++kb, ++s) {
+                        const bool early = s - s_begin < first;
+                        uint8_t* sa = smem + stage * C::STAGE;
+                        if (pass == 1 && !early && !mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                            ok = false;
+                            break;
+                        }
+                        if (pass == 0 || !early) {
+                            mbar_arrive_expect_tx(&full_bar[stage], kBM * kBKB + boxes * 16 * kBKB);
+                            tma_load_2d(sa, &tmW, &full_bar[stage], kb * kBKB, row);
+                            issued |= 1u << stage;
+                            last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                        }
+                        if (pass == 1)
+                            for (int b = 0; b < boxes; ++b)
+                                tma_load_2d(sa + kBM * kBKB + b * 16 * kBKB, &tmH, &full_bar[stage], kb * kBKB, base + b * 16);
+                        if (++stage == C::STAGES) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+            }
+            if (!ok)
+                for (int t = 0; t < C::STAGES; ++t)
+                    if (issued & (1u << t)) mbar_wait(&full_bar[t], (last_par >> t) & 1, nullptr, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one()) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int s = s_begin; s < s_end && ok;) {
+                const int v = s / p.kb2, k0 = s - v * p.kb2;
+                const int k1 = min(p.kb2, k0 + s_end - s);
+                const int cnt = __popcll(__ldcg(p.mask + v % active));
+                const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                        !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_addr(smem + stage * C::STAGE);
+                    const uint64_t ad = sdesc_kmajor_sw128(sa), bd = sdesc_kmajor_sw128(sa + kBM * kBKB);
+#pragma unroll
+                    for (int ks = 0; ks < kBKB / 32; ++ks)
+                        mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    tc_commit(&tfull_bar[buf]);
+                    tc_commit(&empty_bar[stage]);
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    buf ^= 1;
+                    if (buf == 0) bphase ^= 1;
+                }
+                s += k1 - k0;
+            }
+            if (!ok) {
+                tc_commit(&drain_bar);
+                mbar_wait(&drain_bar, 0, nullptr, nullptr);
+            }
+        }
+        __syncwarp();
+    } else {
+        pdl_wait();
+        const int q = warp & 3;
+        const int ch = q * 32 + lane;
+        float* cs = col_s[q];
+        float* oc = out + ch;
+        if (active == 0) {                           // no token chose an expert: y is zero
+            for (int nt = cta; nt < p.ht; nt += static_cast<int>(gridDim.x))
+                if (nt * kBM + ch < p.hidden)
+                    for (int t = 0; t < p.m; ++t) p.y[t * p.ldy + nt * kBM + ch] = __float2bfloat16_rn(0.f);
+        }
+        int buf = 0;
+        uint32_t bphase = 0;
+        bool ok = true;   // as in the up projection
+        for (int s = s_begin; s < s_end;) {
+            // One output tile, or this CTA's piece of it.
+            const int nt = s / tile_steps;
+            const int tile0 = nt * tile_steps, tile1 = tile0 + tile_steps;
+            const int s0 = s, s1 = min(tile1, s_end);
+            for (int t = 0; t < p.m; ++t) oc[t * kBM] = 0.f;
+            while (s < s1) {
+                const int v = s / p.kb2, k0 = s - v * p.kb2;
+                const int k1 = min(p.kb2, k0 + s1 - s);
+                const int a = v - nt * active;
+                const int e = __ldcg(p.expert + a), base = __ldcg(p.base + a);
+                const int cnt = __popcll(__ldcg(p.mask + a));
+                const float* sw = p.s2 + (static_cast<int64_t>(e) * p.ht + nt) * p.kb2;
+                float2 acc[NT / 2];
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+                constexpr int NS = (NT + 31) / 32;
+                float sh[NS], swk = __ldg(sw + k0);
+                auto fetch = [&](int kb) {
+#pragma unroll
+                    for (int c = 0; c < NS; ++c) {
+                        const int i = c * 32 + lane;
+                        sh[c] = i < cnt ? __ldcg(p.hs + static_cast<int64_t>(kb) * p.rows_max + base + i) : 0.f;
+                    }
+                };
+                fetch(k0);
+                for (int kb = k0; kb < k1; ++kb) {
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < NS; ++c)
+                        if (c * 32 + lane < NT) cs[c * 32 + lane] = sh[c] * swk;
+                    if (kb + 1 < k1) {
+                        fetch(kb + 1);
+                        swk = __ldg(sw + kb + 1);
+                    }
+                    ok = ok && mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
+#pragma unroll
+                    for (int c = 0; c < NT / 16; ++c) {
+                        if (c * 16 < cnt) {
+                            uint32_t r[16];
+                            tmem_ld16(tb + c * 16, r);
+                            tmem_ld_wait();
+                            promote16(acc + c * 8, r, cs + c * 16);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                    buf ^= 1;
+                    if (buf == 0) bphase ^= 1;
+                }
+                // The expert's weighted rows join the tile's sums (a thread owns its channel).
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (i < cnt) {
+                        const int t = __ldcg(p.row_token + base + i);
+                        const float wt = __ldcg(p.row_weight + base + i);
+                        oc[t * kBM] = __fmaf_rn(wt, (i & 1) ? acc[i / 2].y : acc[i / 2].x, oc[t * kBM]);
+                    }
+                }
+                s += k1 - k0;
+            }
+            bool finish = true;
+            int first = cta, lastc = cta;
+            if (s1 - s0 < tile_steps) {
+                float* mine = p.part + (static_cast<int64_t>(cta) * 2 + (s0 > tile0 ? 0 : 1)) * (p.m * kBM) + ch;
+                for (int t = 0; t < p.m; ++t) mine[t * kBM] = oc[t * kBM];
+                first = line.owner(tile0);
+                lastc = line.owner(tile1 - 1);
+                finish = arrive_last(&p.down_count[nt], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1, 128);
+                if (finish) {
+                    for (int t = 0; t < p.m; ++t) oc[t * kBM] = 0.f;
+                    for (int c = first; c <= lastc; ++c) {
+                        const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) + ch;
+                        for (int t = 0; t < p.m; ++t) oc[t * kBM] += __ldcg(src + t * kBM);
+                    }
+                }
+            }
+            if (finish && nt * kBM + ch < p.hidden)
+                for (int t = 0; t < p.m; ++t)
+                    p.y[t * p.ldy + nt * kBM + ch] = __float2bfloat16_rn(oc[t * kBM]);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+// ============================================================================
+// Host side
+// ============================================================================
+template <typename T>
+cudaError_t route(const MoeRouteArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.m + 3) / 4), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_route_kernel<T>, static_cast<const T*>(a.logits), a.ld, a.m,
+                              static_cast<int>(a.experts), static_cast<int>(a.top_k), a.sigmoid ? 1 : 0,
+                              a.renormalize ? 1 : 0, a.ids, a.weights);
+}
+
+// The workspace, cut up in this order; returns its size (base may be null).
+int64_t layout(const MoeLayerArgs& a, uint8_t* base, MoeParams* p) {
+    auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    const int64_t rows = a.m * a.top_k, act = a.experts < rows ? a.experts : rows;
+    const int64_t it = a.inter / kBlock, ht = (a.hidden + kBlock - 1) / kBlock;
+    const int64_t nt = a.m <= 16 ? 16 : a.m <= 32 ? 32 : 64;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        uint8_t* r = base + at;
+        at += up(bytes);
+        return r;
+    };
+    uint8_t* head = take(8);
+    uint8_t* expert = take(4 * act);
+    uint8_t* first = take(4 * act);
+    uint8_t* mask = take(8 * act);
+    uint8_t* token = take(4 * rows);
+    uint8_t* weight = take(4 * rows);
+    uint8_t* upc = take(4 * act * it);
+    uint8_t* downc = take(4 * ht);
+    uint8_t* xq = take(a.m * a.hidden);
+    uint8_t* xs = take(4 * a.m * ht);
+    uint8_t* hq = take(rows * a.inter);
+    uint8_t* hs = take(4 * rows * it);
+    // The up projection's sums are dead before the down projection writes its own.
+    const int64_t part_up = 4 * 2 * nt * kBM, part_down = 4 * a.m * kBM;
+    uint8_t* part = take(2 * kMoeMaxCtas * (part_up > part_down ? part_up : part_down));
+    if (p) {
+        p->m = static_cast<int>(a.m);
+        p->top_k = static_cast<int>(a.top_k);
+        p->experts = static_cast<int>(a.experts);
+        p->hidden = static_cast<int>(a.hidden);
+        p->inter = static_cast<int>(a.inter);
+        p->rows_max = static_cast<int>(rows);
+        p->it = p->kb2 = static_cast<int>(it);
+        p->ht = p->kb1 = static_cast<int>(ht);
+        p->head = reinterpret_cast<int*>(head);
+        p->expert = reinterpret_cast<int*>(expert);
+        p->base = reinterpret_cast<int*>(first);
+        p->mask = reinterpret_cast<unsigned long long*>(mask);
+        p->row_token = reinterpret_cast<int*>(token);
+        p->row_weight = reinterpret_cast<float*>(weight);
+        p->up_count = reinterpret_cast<int*>(upc);
+        p->down_count = reinterpret_cast<int*>(downc);
+        p->xq = xq;
+        p->xs = reinterpret_cast<float*>(xs);
+        p->hq = hq;
+        p->hs = reinterpret_cast<float*>(hs);
+        p->part = reinterpret_cast<float*>(part);
+        p->s13 = a.s13;
+        p->s2 = a.s2;
+        p->y = a.y;
+        p->ldy = a.ldy;
+        p->status = device_status_ptr();
+    }
+    return at;
+}
+
+template <typename K, typename... Args>
+q8_status launch(K kern, int blocks, int threads, int smem, cudaStream_t s, Args... args) {
+    if (smem > 0 && set_smem(kern, smem) != cudaSuccess) return Q8_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return Q8_ERR_LAUNCH;
+    }
+    return Q8_OK;
+}
+
+template <typename T>
+q8_status prepare(const MoeLayerArgs& a, const MoeParams& p, cudaStream_t s) {
+    return launch(moe_prepare_kernel<T>, static_cast<int>((a.hidden + 255) / 256) + 1, 256, 0, s,
+                  static_cast<const T*>(a.x), a.ldx, a.ids, a.weights, p);
+}
+
+template <int NT>
+q8_status products(const MoeLayerArgs& a, const MoeParams& p, cudaStream_t s) {
+    CUtensorMap tW13, tX, tW2, tH;
+    if (!make_map(&tW13, a.w13, false, a.hidden, a.experts * 2 * a.inter, a.ld13, kBKB, kBM) ||
+        !make_map(&tX, p.xq, false, a.hidden, a.m, a.hidden, kBKB, NT) ||
+        !make_map(&tW2, a.w2, false, a.inter, a.experts * a.hidden, a.ld2, kBKB, kBM) ||
+        !make_map(&tH, p.hq, false, a.inter, p.rows_max, a.inter, kBKB, 16))
+        return Q8_ERR_CUDA;
+    const int ctas = sm_count() < kMoeMaxCtas ? sm_count() : static_cast<int>(kMoeMaxCtas);
+    const q8_status st = launch(moe_up_kernel<NT>, ctas, MoeUpCfg<NT>::THREADS, MoeUpCfg<NT>::SMEM, s, tW13, tX, p);
+    if (st != Q8_OK) return st;
+    return launch(moe_down_kernel<NT>, ctas, MoeDownCfg<NT>::THREADS, MoeDownCfg<NT>::SMEM, s, tW2, tH, p);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const MoeRouteArgs& a, cudaStream_t s) {
+    switch (a.dtype) {
+        case Q8_F16: return route<__half>(a, s);
+        case Q8_BF16: return route<__nv_bfloat16>(a, s);
+        default: return route<float>(a, s);
+    }
+}
+
+int64_t moe_workspace_bytes(const MoeLayerArgs& a) { return layout(a, nullptr, nullptr); }
+
+q8_status launch_moe_layer(const MoeLayerArgs& a, uint8_t* workspace, cudaStream_t s) {
+    MoeParams p = {};
+    layout(a, workspace, &p);
+    q8_status st;
+    switch (a.x_dtype) {
+        case Q8_F16: st = prepare<__half>(a, p, s); break;
+        case Q8_BF16: st = prepare<__nv_bfloat16>(a, p, s); break;
+        default: st = prepare<float>(a, p, s); break;
+    }
+    if (st != Q8_OK) return st;
+    if (a.m <= 16) return products<16>(a, p, s);
+    if (a.m <= 32) return products<32>(a, p, s);
+    return products<64>(a, p, s);
+}
+
+}  // namespace q8

@@ -33,6 +33,7 @@ Q8_ERR_UNSUPPORTED_ARCH, Q8_ERR_LAUNCH, Q8_ERR_DEVICE_TIMEOUT, Q8_ERR_WORKSPACE,
 Q8_S8, Q8_U8, Q8_E4M3, Q8_F16, Q8_BF16, Q8_F32, Q8_S32 = range(7)
 Q8_ASYM_INT8, Q8_SYM_INT8, Q8_FP8_E4M3 = range(3)
 Q8_OP_LINEAR_W8A8, Q8_OP_LINEAR_INT8_MIXED, Q8_OP_LINEAR_FP8_BLOCK = 0, 1, 2
+Q8_SOFTMAX, Q8_SIGMOID = 0, 1
 Q8_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTED = [
@@ -45,6 +46,7 @@ EXPORTED = [
     "q8_linear_fp8_grouped",
     "q8_quantize_act_block", "q8_quantize_weight_block",
     "q8_linear_fp8_block", "q8_linear_fp8_block_dynamic", "q8_linear_fp8_block_grouped",
+    "q8_moe_route", "q8_moe_fp8_block", "q8_moe_workspace_size",
     "q8_workspace_size", "q8_status_string",
     "q8_get_device_status", "q8_clear_device_status", "q8_device_check", "q8_version",
     "q8_inject_failure", "q8_selftest_wait_timeout",
@@ -114,6 +116,10 @@ _SIG = {
                                      _vp, _vp, _i64, _vp, _sz, _vp], _int),
     "q8_linear_fp8_block_grouped": ([ctypes.POINTER(CActBlock), ctypes.POINTER(CWeightBlock), _i64,
                                      _vp, _vp, _vp, _i64, _vp], _int),
+    "q8_moe_route": ([_vp, _int, _i64, _i64, _i64, _i64, _int, ctypes.c_int32, _vp, _vp, _vp], _int),
+    "q8_moe_fp8_block": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(CWeightBlock),
+                          ctypes.POINTER(CWeightBlock), _i64, _vp, _i64, _vp, _sz, _vp], _int),
+    "q8_moe_workspace_size": ([_i64] * 5, _sz),
     "q8_workspace_size": ([_int, _i64, _i64, _i64], _sz),
     "q8_status_string": ([_int], ctypes.c_char_p),
     "q8_get_device_status": ([_vp, _vp], _int),
@@ -695,6 +701,71 @@ def q8_linear_fp8_block_grouped(x: QActBlock, w: QWeightBlock, offsets: torch.Te
     _on(dev, _lib.q8_linear_fp8_block_grouped, made, stream, "q8_linear_fp8_block_grouped",
         (ctypes.byref(cx), ctypes.byref(cw), e, offsets.data_ptr(), _ptr(bias), out.data_ptr(), _ld(out)),
         ((w.codes, "w"),))
+    return out
+
+
+_SCORING = {"softmax": Q8_SOFTMAX, "sigmoid": Q8_SIGMOID}
+
+
+def q8_moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", renormalize: bool = True,
+                 out=None, stream=None):
+    """The router's top-k choice (see q8_moe_route in q8.h): (ids int32 m x top_k, weights fp32 m x top_k)."""
+    _cuda(logits, "logits")
+    m, experts = logits.shape
+    dev = logits.device
+    made = ()
+    if out is None:
+        out = made = (torch.empty((m, top_k), dtype=torch.int32, device=dev),
+                      torch.empty((m, top_k), dtype=torch.float32, device=dev))
+    ids, weights = out
+    _check_choice(ids, weights, m, top_k, dev)
+    _on(dev, _lib.q8_moe_route, made, stream, "q8_moe_route",
+        (logits.data_ptr(), _FLOAT_DT.get(logits.dtype, -1), m, experts, _ld(logits), top_k,
+         _SCORING.get(scoring, -1), int(renormalize), ids.data_ptr(), weights.data_ptr()))
+    return ids, weights
+
+
+def _check_choice(ids, weights, m, top_k, device):
+    if (ids.device != device or ids.dtype != torch.int32 or ids.shape != (m, top_k) or not ids.is_contiguous()
+            or weights.device != device or weights.dtype != torch.float32 or weights.shape != (m, top_k)
+            or not weights.is_contiguous()):
+        raise ValueError(f"ids and weights must be contiguous int32 and float32 tensors of shape {(m, top_k)} on {device}")
+
+
+def q8_moe_workspace_size(m: int, top_k: int, num_experts: int, hidden: int, inter: int) -> int:
+    return int(_lib.q8_moe_workspace_size(m, top_k, num_experts, hidden, inter))
+
+
+def q8_moe_fp8_block(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: QWeightBlock,
+                     w2: QWeightBlock, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The whole expert layer for up to 64 tokens: w13 a stack experts x 2 inter x hidden (gate rows,
+    then up rows), w2 a stack experts x hidden x inter, ids and weights as q8_moe_route gives them;
+    returns bf16 m x hidden."""
+    _cuda(X, "X")
+    m, hidden = X.shape
+    dev = X.device
+    c13, c2 = w13.c(), w2.c()
+    experts = w13.experts
+    if w2.experts != experts:
+        raise ValueError("w13 and w2 must hold the same number of experts")
+    top_k = ids.shape[1] if ids.dim() == 2 else 0
+    _check_choice(ids, weights, m, top_k, dev)
+    made = []
+    if out is None:
+        out = torch.empty((m, hidden), dtype=torch.bfloat16, device=dev)
+        made.append(out)
+    else:
+        _check_out(out, (m, hidden), torch.bfloat16, dev)
+    if workspace is None:
+        need = q8_moe_workspace_size(m, top_k, experts, hidden, c2.k)
+        workspace = torch.empty(need if need < 1 << 62 else 0, dtype=torch.uint8, device=dev)
+        made.append(workspace)
+    _on(dev, _lib.q8_moe_fp8_block, made, stream, "q8_moe_fp8_block",
+        (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, hidden, _ld(X), ids.data_ptr(), weights.data_ptr(), top_k,
+         ctypes.byref(c13), ctypes.byref(c2), experts, out.data_ptr(), _ld(out), _ptr(workspace),
+         workspace.numel() * workspace.element_size()),
+        ((w13.codes, "w13"), (w2.codes, "w2"), (workspace, "workspace")))
     return out
 
 

@@ -15,7 +15,8 @@
  *     multiplied with 16-bit activations (W4A16);
  *   - the grouped FP8 rowwise linear of mixture-of-experts layers;
  *   - block-scaled FP8 (one scale per 128 values of a token and per 128 x 128
- *     block of a weight): quantizers, linear, grouped linear.
+ *     block of a weight): quantizers, linear, grouped linear, the router's
+ *     choice and the whole expert layer for a few tokens.
  *
  * Notation follows the pages' linear map Q = round(R / S) + Z, R = S (Q - Z):
  * `scale` is S, the dequant multiplier, and `zero_point` is Z, an integer held
@@ -586,6 +587,74 @@ q8_status q8_linear_fp8_block_dynamic(const void *X, q8_dtype x_dtype, int64_t m
 q8_status q8_linear_fp8_block_grouped(const q8_act_block *x, const q8_weight_block *w,
                                       int64_t num_experts, const int32_t *offsets, const float *bias,
                                       void *Y, int64_t ldy, q8_stream_t stream);
+
+typedef enum {
+    Q8_SOFTMAX = 0,  /* exp(l) / sum of exp(l) */
+    Q8_SIGMOID = 1   /* 1 / (1 + exp(-l)) */
+} q8_scoring;
+
+/*
+ * The router's choice for a mixture-of-experts layer: per token the top_k
+ * largest logits, the lowest expert index first among equals, in descending
+ * order ([FBGEMM] 5.4, Llama4 experts: each token goes to its experts).
+ *   logits       device, m x num_experts, Q8_F32, Q8_BF16 or Q8_F16, row
+ *                stride ld (aligned to its element).  -inf and NaN are never
+ *                chosen (masked experts); +inf counts as the largest fp32.
+ *   num_experts  1 .. 512;  top_k 1 .. min(16, num_experts).
+ *   scoring      weights are the softmax over all experts, or the sigmoid of
+ *                the chosen logits (Q8_ERR_SCHEME otherwise).
+ *   renormalize  non-zero: the chosen weights are divided by their sum (0
+ *                where that is 0).
+ *   ids          device int32 [m][top_k] output; -1 where a token has fewer
+ *                than top_k experts that may be chosen.
+ *   weights      device fp32 [m][top_k] output; 0 where ids is -1.
+ * One launch.
+ */
+q8_status q8_moe_route(const void *logits, q8_dtype dtype, int64_t m, int64_t num_experts, int64_t ld,
+                       int64_t top_k, q8_scoring scoring, int32_t renormalize, int32_t *ids,
+                       float *weights, q8_stream_t stream);
+
+/*
+ * A whole expert layer for a few tokens (decode), on block-scaled FP8
+ * weights: for every token t and each of its experts e = ids[t, s]
+ *   G, U = gate and up rows of W13[e] times q(x_t)
+ *   h = q(fl32(G / (1 + exp(-G)) * U))
+ *   y_t = sum_s weights[t, s] * (W2[e] h),  Y = bf16_rne(y)
+ * with q the quantizer of q8_quantize_act_block and the products and sums of
+ * q8_linear_fp8_block (h and the sums over experts stay in fp32 up to q and
+ * the final rounding).  Results repeat bit for bit.  Only the chosen experts'
+ * weights are read.
+ *   X           device, m x hidden, Q8_F16, Q8_BF16 or Q8_F32, row stride ldx;
+ *               m <= 64 (longer batches: sort the tokens by expert and use
+ *               q8_linear_fp8_block_grouped).
+ *   ids         device int32 [m][top_k], e.g. from q8_moe_route.  Entries
+ *               outside [0, num_experts) are skipped (a token without any
+ *               expert gets zeros); an expert that a token names twice counts
+ *               with both weights.
+ *   weights     device fp32 [m][top_k].
+ *   w13         stack of num_experts weights of 2 * inter rows (the inter gate
+ *               rows, then the inter up rows) and hidden columns.
+ *   w2          stack of num_experts weights of hidden rows, inter columns.
+ *               inter % 128 == 0, hidden % 32 == 0, both <= 65536;
+ *               num_experts <= 512, top_k <= 16.
+ *   Y           device, m x hidden bf16, row stride ldy (ldy % 8 == 0).
+ *   workspace   at least q8_moe_workspace_size(...) bytes, 256-byte aligned;
+ *               needs no initialization.  Calls that overlap on the GPU need
+ *               one each.
+ * Three launches (x and the expert list, gate and up, down), chained by
+ * programmatic dependent launch; the launch-overlap rule of q8_linear_w8a8
+ * applies to codes and scales of the weights.
+ */
+q8_status q8_moe_fp8_block(const void *X, q8_dtype x_dtype, int64_t m, int64_t hidden, int64_t ldx,
+                           const int32_t *ids, const float *weights, int64_t top_k,
+                           const q8_weight_block *w13, const q8_weight_block *w2,
+                           int64_t num_experts, void *Y, int64_t ldy, void *workspace,
+                           size_t ws_bytes, q8_stream_t stream);
+
+/* Bytes of device workspace q8_moe_fp8_block needs (host function, no device
+ * access); SIZE_MAX for sizes that no call takes, 0 for negative ones. */
+size_t q8_moe_workspace_size(int64_t m, int64_t top_k, int64_t num_experts, int64_t hidden,
+                             int64_t inter);
 
 enum { Q8_OP_LINEAR_W8A8 = 0, Q8_OP_LINEAR_INT8_MIXED = 1, Q8_OP_LINEAR_FP8_BLOCK = 2 };
 
