@@ -185,7 +185,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
 
-    const int warp = threadIdx.x / 32;
+    const int warp = warp_index();
     const int lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();          // 0: issues the pair's MMAs
     const int pair = static_cast<int>(blockIdx.x >> 1);
@@ -239,12 +239,11 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             if constexpr (!GROUPED) {
                 if (pair < num_tiles) {
                     const TileRef tr0 = tile_ref(pair);
-                    const int yb0 = tr0.b_row + static_cast<int>(rank) * (BN / 2);
                     npre = num_kb < C::STAGES ? num_kb : C::STAGES;
                     for (int s = 0; s < npre; ++s) {
                         if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * C::STAGE);
                         tma_load_2d_pair(smem + s * C::STAGE + C::A_BYTES, &tmB, full0 + 8u * static_cast<uint32_t>(s),
-                                         s * kBKB, yb0);
+                                         s * kBKB, tr0.b_row + static_cast<int>(rank) * (BN / 2));
                     }
                 }
             }
@@ -257,7 +256,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                 const TileRef tr = tile_ref(tile);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     const bool pre = tile == pair && kb < npre;   // weight half already out
-                    if (!pre && !mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                    if (!pre && !mbar_wait_short(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
@@ -286,15 +285,19 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
     } else if (warp == 1) {
         reg_dealloc<kPairRegsLow>();
         // ------------------------------------------------ MMA issuer (even CTA)
-        if (rank == 0 && elect_one()) {
+        if (rank == 0) {
+            // The whole warp runs the loop and one lane issues: descriptors then
+            // stay in uniform registers, without which an MMA takes about 75
+            // cycles to issue and the issue bounds the kernel.
+            const bool leader = elect_one();
             const uint32_t idesc = make_idesc(1, 0, 0, 2 * kBM, BN);
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
             for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                        !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
@@ -303,11 +306,14 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     const uint32_t sa = smem_addr(smem + stage * C::STAGE);
                     const uint64_t ad = sdesc_kmajor_sw128(sa);
                     const uint64_t bd = sdesc_kmajor_sw128(sa + C::A_BYTES);
+                    if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < kBKB / 32; ++ks)
-                        mma_issue_pair<kKindF8>(d, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-                    tc_commit_pair(&tfull_bar[buf], 0x3);
-                    tc_commit_pair(&empty_bar[stage], 0x3);
+                        for (int ks = 0; ks < kBKB / 32; ++ks)
+                            mma_issue_pair<kKindF8>(d, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                        tc_commit_pair(&tfull_bar[buf], 0x3);
+                        tc_commit_pair(&empty_bar[stage], 0x3);
+                    }
+                    __syncwarp();
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -316,7 +322,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     if (buf == 0) bphase ^= 1;
                 }
             }
-            if (!ok) {
+            if (!ok && leader) {
                 // Abort: wait for the MMAs already issued before TMEM is freed.
                 tc_commit_pair_local(&drain_bar);
                 mbar_wait(&drain_bar, 0, nullptr, nullptr);
@@ -350,51 +356,54 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             float2 acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            // Scales are fetched four groups ahead of their use.
-            float s_cur[4], s_nxt[4];
+            // Scales are fetched four groups ahead of their use.  The loads are
+            // volatile and the products are formed at the use: left to itself,
+            // the compiler forms them right behind the loads, and every fourth
+            // group then waits about 2000 cycles for memory.
+            float a_cur[4], b_cur[4];
+            auto fetch = [&](int kb, float& a, float& b) {
+                const int k = kb < num_kb ? kb : num_kb - 1;   // past the end: loaded, not used
+                a = ldg_volatile(sx + static_cast<int64_t>(k) * p.m);
+                b = ldg_volatile(sw + k);
+            };
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                s_cur[j] = j < num_kb ? sx[static_cast<int64_t>(j) * p.m] * sw[j] : 0.f;
+            for (int j = 0; j < 4; ++j) fetch(j, a_cur[j], b_cur[j]);
             for (int kb0 = 0; kb0 < num_kb && ok; kb0 += 4) {
-                float a_n[4], b_n[4];
+                float a_nxt[4], b_nxt[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int kb = kb0 + 4 + j;
-                    a_n[j] = kb < num_kb ? __ldg(sx + static_cast<int64_t>(kb) * p.m) : 0.f;
-                    b_n[j] = kb < num_kb ? __ldg(sw + kb) : 0.f;
-                }
+                for (int j = 0; j < 4; ++j) fetch(kb0 + 4 + j, a_nxt[j], b_nxt[j]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (kb0 + j >= num_kb) break;
-                    if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) {
+                    if (!mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
                     __syncwarp();
                     tc_fence_after();
+                    const float sc = a_cur[j] * b_cur[j];
                     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * C::CW;
-                    uint32_t r[2][16];
-                    tmem_ld16(tb, r[0]);
 #pragma unroll
-                    for (int c = 0; c < C::CW / 16; ++c) {
+                    for (int c = 0; c < C::CW / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(tb + c * 32, r);
                         tmem_ld_wait();
-                        if (c + 1 < C::CW / 16) {
-                            tmem_ld16(tb + (c + 1) * 16, r[(c + 1) & 1]);
-                        } else {
+                        if (c + 1 == C::CW / 32) {
                             // All of this warp's part is in registers: the buffer may be written again.
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive_cluster_no_fence(tempty0 + 8u * static_cast<uint32_t>(buf));
                         }
-                        promote16(acc + c * 8, r[c & 1], s_cur[j]);
+                        promote(acc + c * 16, r, sc);
                     }
                     buf ^= 1;
                     if (buf == 0) bphase ^= 1;
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s_nxt[j] = a_n[j] * b_n[j];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s_cur[j] = s_nxt[j];
+                for (int j = 0; j < 4; ++j) {
+                    a_cur[j] = a_nxt[j];
+                    b_cur[j] = b_nxt[j];
+                }
             }
             if (!ok) break;
             // A tensor store clips at the output's last row only: chunks that
@@ -520,7 +529,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     __shared__ float sx_ring[QX ? C::SX_RING : 1][QX ? NT : 1];
     __shared__ __align__(8) uint64_t sx_bar[QX ? C::SX_RING : 1];  // every quad of the slot is written
 
-    const int warp = threadIdx.x / 32;
+    const int warp = warp_index();
     const int lane = threadIdx.x % 32;
     const int tn = blockIdx.x;                       // 128 output channels
     const int t0 = static_cast<int>(blockIdx.z) * NT;
@@ -579,7 +588,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             uint32_t phase = first == nstages ? 1u : 0u;
             bool ok = true;
             for (int kb = kb0 + first; kb < kb1; ++kb) {
-                if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                if (!mbar_wait_short(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
                     ok = false;
                     break;
                 }
@@ -600,14 +609,15 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
+        {
+            const bool leader = elect_one();   // one lane issues, as in the pair kernel
             const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((mt + 15) / 16 * 16));
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
             for (int i = 0; i < my_kb; ++i) {
-                if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                    !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                    !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
                     ok = false;
                     break;
                 }
@@ -615,11 +625,14 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                 const uint32_t sa = smem_addr(smem + stage * C::STAGE);
                 const uint64_t ad = sdesc_kmajor_sw128(sa);
                 const uint64_t bd = sdesc_kmajor_sw128(sa + C::A_BYTES);
+                if (leader) {
 #pragma unroll
-                for (int ks = 0; ks < kBKB / 32; ++ks)
-                    mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-                tc_commit(&tfull_bar[buf]);
-                tc_commit(&empty_bar[stage]);
+                    for (int ks = 0; ks < kBKB / 32; ++ks)
+                        mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    tc_commit(&tfull_bar[buf]);
+                    tc_commit(&empty_bar[stage]);
+                }
+                __syncwarp();
                 if (++stage == nstages) {
                     stage = 0;
                     phase ^= 1;
@@ -627,7 +640,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                 buf ^= 1;
                 if (buf == 0) bphase ^= 1;
             }
-            if (!ok) {
+            if (!ok && leader) {
                 tc_commit(&drain_bar);
                 mbar_wait(&drain_bar, 0, nullptr, nullptr);
             }
@@ -661,7 +674,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         for (int i = 0; i < my_kb; ++i) {
             const int kb = kb0 + i;
             if constexpr (QX) {
-                if (!mbar_wait(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
+                if (!mbar_wait_short(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
                 if (lane < C::CW) cs[lane] = lane < cn ? sx_ring[i % C::SX_RING][lane] * swk : 0.f;
             } else {
 #pragma unroll
@@ -672,7 +685,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                 if (i + 1 < my_kb) fetch_sx(kb + 1);
             }
             if (i + 1 < my_kb) swk = __ldg(sw + kb + 1);
-            if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
+            if (!mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
             __syncwarp();
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + c0;
@@ -731,7 +744,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             const uint4 w = quantize16<T>(lo, hi, s);
             if (piece + kQxWarps < pieces) load(piece + kQxWarps, lo, hi);
             const int stage = i % nstages, use = i / nstages;
-            if (use > 0 && !mbar_wait(&empty_bar[stage], (use - 1) & 1, &abort_sh, p.status)) break;
+            if (use > 0 && !mbar_wait_short(&empty_bar[stage], (use - 1) & 1, &abort_sh, p.status)) break;
             __syncwarp();
             st_shared_v4(smem + stage * C::STAGE + C::A_BYTES + t * kBKB + ((sub ^ (t & 7)) << 4), w.x, w.y, w.z, w.w);
             if (sub == 0) sx_ring[i % C::SX_RING][t] = s;

@@ -83,6 +83,12 @@ struct Eight<float> {
     }
 };
 
+__device__ __forceinline__ float ldg_volatile(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ float absmax8(const float (&f)[8]) {
     float m = fabsf(f[0]);
 #pragma unroll
@@ -106,15 +112,25 @@ __device__ __forceinline__ uint4 quantize16(const Eight<T>& lo, const Eight<T>& 
                       block_codes4(b[0], b[1], b[2], b[3], s), block_codes4(b[4], b[5], b[6], b[7], s));
 }
 
-// acc[i] += s * part[i] for 16 accumulator columns in registers, with one scale.
-__device__ __forceinline__ void promote16(float2* acc, const uint32_t (&r)[16], float s) {
-    const float2 s2 = make_float2(s, s);
+// acc[i] += s * part[i] for 32 accumulator columns in registers, with one
+// scale.  Volatile, so that the additions stay before the next tensor-memory
+// load: moved behind it, they keep both loads' registers alive and spill.
+__device__ __forceinline__ void promote(float2* acc, const uint32_t (&r)[32], float s) {
+    unsigned long long s2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        acc[i] = __ffma2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), s2, acc[i]);
+    for (int i = 0; i < 16; ++i)
+        asm volatile(
+            "{\n\t.reg .b64 p, a;\n\t"
+            "mov.b64 p, {%2, %3};\n\t"
+            "mov.b64 a, {%0, %1};\n\t"
+            "fma.rn.f32x2 a, p, %4, a;\n\t"
+            "mov.b64 {%0, %1}, a;\n\t}"
+            : "+f"(acc[i].x), "+f"(acc[i].y)
+            : "r"(r[2 * i]), "r"(r[2 * i + 1]), "l"(s2));
 }
 
-// The same with a scale per column, from 16-byte-aligned shared memory.
+// The same for 16 columns with a scale per column, from 16-byte-aligned shared memory.
 __device__ __forceinline__ void promote16(float2* acc, const uint32_t (&r)[16], const float* s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

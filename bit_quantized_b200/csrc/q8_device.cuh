@@ -84,6 +84,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     }
 }
 
+// mbar_wait for waits that are short and on the critical path, such as the
+// hand-over of an accumulator for every 128 values of K: the abort flag and the
+// clock (whose reads cost hundreds of cycles) come in only after some polls.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                int* status) {
+    const uint32_t a = smem_addr(bar);
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(a, parity)) return true;
+    return mbar_wait(bar, parity, abort_flag, status);
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
@@ -411,6 +423,12 @@ __device__ __forceinline__ void reg_dealloc() {
 template <int N>
 __device__ __forceinline__ void reg_alloc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// The warp's index in the block, known to the compiler to be the same in every
+// lane, so that a branch on it is a uniform one.
+__device__ __forceinline__ int warp_index() {
+    return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
 }
 
 __device__ __forceinline__ bool elect_one() {

@@ -153,7 +153,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restrict__ ids,
                    const float* __restrict__ weights, const MoeParams p) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = warp_index(), lane = threadIdx.x % 32;
     if (blockIdx.x + 1 < gridDim.x) {
         // 256 columns (two groups) of every token; a warp takes a token at a time.
         const int col = static_cast<int>(blockIdx.x) * 256 + lane * 8;
@@ -309,7 +309,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     __shared__ __align__(16) float col_s[C::PROMO][2][C::CW];
     __shared__ float amax_sh[C::HALVES][4][C::CW];
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = warp_index(), lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
@@ -356,7 +356,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const int a = u / p.it;
                 const int row = p.expert[a] * 2 * p.inter + (u - a * p.it) * kBM;
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                    if (!mbar_wait_short(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
@@ -380,14 +380,17 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
+        {
+            // The whole warp runs the loop and one lane issues: descriptors then
+            // stay in uniform registers.
+            const bool leader = elect_one();
             const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((p.m + 15) / 16 * 16));
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
             for (int s = s_begin; s < s_end; ++s) {
-                if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                    !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                    !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
                     ok = false;
                     break;
                 }
@@ -396,13 +399,16 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const uint64_t gd = sdesc_kmajor_sw128(sa), ud = sdesc_kmajor_sw128(sa + kBM * kBKB);
                 const uint64_t bd = sdesc_kmajor_sw128(sa + 2 * kBM * kBKB);
                 const uint32_t d = tmem_base + buf * 2 * NT;
+                if (leader) {
 #pragma unroll
-                for (int ks = 0; ks < kBKB / 32; ++ks) {
-                    mma_issue<kKindF8>(d, gd + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-                    mma_issue<kKindF8>(d + NT, ud + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    for (int ks = 0; ks < kBKB / 32; ++ks) {
+                        mma_issue<kKindF8>(d, gd + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                        mma_issue<kKindF8>(d + NT, ud + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    }
+                    tc_commit(&tfull_bar[buf]);
+                    tc_commit(&empty_bar[stage]);
                 }
-                tc_commit(&tfull_bar[buf]);
-                tc_commit(&empty_bar[stage]);
+                __syncwarp();
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1;
@@ -410,7 +416,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 buf ^= 1;
                 if (buf == 0) bphase ^= 1;
             }
-            if (!ok) {
+            if (!ok && leader) {
                 tc_commit(&drain_bar);
                 mbar_wait(&drain_bar, 0, nullptr, nullptr);
             }
@@ -453,7 +459,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     wg = __ldg(sg + kb + 1);
                     wu = __ldg(su + kb + 1);
                 }
-                ok = ok && mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status);
+                ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -577,7 +583,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     __shared__ int abort_sh, last_sh;
     __shared__ __align__(16) float col_s[4][NT];
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = warp_index(), lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
@@ -633,7 +639,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     for (int kb = k0; kb < k1; ++kb, ++s) {
                         const bool early = s - s_begin < first;
                         uint8_t* sa = smem + stage * C::STAGE;
-                        if (pass == 1 && !early && !mbar_wait(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
+                        if (pass == 1 && !early && !mbar_wait_short(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
                             ok = false;
                             break;
                         }
@@ -659,7 +665,8 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
+        {
+            const bool leader = elect_one();
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
@@ -669,19 +676,22 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 const int cnt = __popcll(__ldcg(p.mask + v % active));
                 const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                        !mbar_wait(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_addr(smem + stage * C::STAGE);
                     const uint64_t ad = sdesc_kmajor_sw128(sa), bd = sdesc_kmajor_sw128(sa + kBM * kBKB);
+                    if (leader) {
 #pragma unroll
-                    for (int ks = 0; ks < kBKB / 32; ++ks)
-                        mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-                    tc_commit(&tfull_bar[buf]);
-                    tc_commit(&empty_bar[stage]);
+                        for (int ks = 0; ks < kBKB / 32; ++ks)
+                            mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                        tc_commit(&tfull_bar[buf]);
+                        tc_commit(&empty_bar[stage]);
+                    }
+                    __syncwarp();
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -691,7 +701,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 }
                 s += k1 - k0;
             }
-            if (!ok) {
+            if (!ok && leader) {
                 tc_commit(&drain_bar);
                 mbar_wait(&drain_bar, 0, nullptr, nullptr);
             }
@@ -746,7 +756,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                         fetch(kb + 1);
                         swk = __ldg(sw + kb + 1);
                     }
-                    ok = ok && mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status);
+                    ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();

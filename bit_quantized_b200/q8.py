@@ -533,15 +533,18 @@ class QWeightBlock:
 
     def c(self) -> CWeightBlock:
         q, S = self.codes, self.scale
-        n, k = q.shape[-2:]
-        if q.dim() not in (2, 3) or not q.is_cuda or q.dtype != torch.float8_e4m3fn or q.stride(-1) != 1:
+        shape, stride = q.shape, q.stride()
+        dims = len(shape)
+        if dims not in (2, 3) or not q.is_cuda or q.dtype is not torch.float8_e4m3fn or stride[-1] != 1:
             raise ValueError("weight codes must be a 2-D or 3-D CUDA float8_e4m3fn tensor with unit column stride")
-        if q.dim() == 3 and q.shape[0] > 1 and q.stride(0) != n * q.stride(1):
+        n, k = shape[-2], shape[-1]
+        experts = shape[0] if dims == 3 else 1
+        if experts > 1 and stride[0] != n * stride[1]:
             raise ValueError("the experts of a weight stack must follow each other without a gap")
-        want = q.shape[:-2] + ((n + 127) // 128, (k + 127) // 128)
-        if S.device != q.device or S.dtype != torch.float32 or S.shape != want or not S.is_contiguous():
-            raise ValueError(f"weight scale must be a contiguous float32 tensor of shape {tuple(want)} on the codes' device")
-        return CWeightBlock(q.data_ptr(), S.data_ptr(), self.experts * n, k, q.stride(-2))
+        want = (experts, (n + 127) // 128, (k + 127) // 128)[3 - dims:]
+        if S.device != q.device or S.dtype is not torch.float32 or S.shape != want or not S.is_contiguous():
+            raise ValueError(f"weight scale must be a contiguous float32 tensor of shape {want} on the codes' device")
+        return CWeightBlock(q.data_ptr(), S.data_ptr(), experts * n, k, stride[-2])
 
 
 @dataclasses.dataclass
@@ -553,12 +556,12 @@ class QActBlock:
 
     def c(self) -> CActBlock:
         q, S = self.codes, self.scale
-        if q.dim() != 2 or not q.is_cuda or q.dtype != torch.float8_e4m3fn or q.stride(1) != 1:
+        if q.dim() != 2 or not q.is_cuda or q.dtype is not torch.float8_e4m3fn or q.stride(1) != 1:
             raise ValueError("activation codes must be a 2-D CUDA float8_e4m3fn tensor with unit column stride")
         m, k = q.shape
-        if S.device != q.device or S.dtype != torch.float32 or S.shape != ((k + 127) // 128, m) or not S.is_contiguous():
-            raise ValueError(f"activation scale must be a contiguous float32 tensor of shape {((k + 127) // 128, m)} "
-                             "on the codes' device")
+        want = ((k + 127) // 128, m)
+        if S.device != q.device or S.dtype is not torch.float32 or S.shape != want or not S.is_contiguous():
+            raise ValueError(f"activation scale must be a contiguous float32 tensor of shape {want} on the codes' device")
         return CActBlock(q.data_ptr(), S.data_ptr(), m, k, q.stride(0))
 
 
@@ -568,21 +571,24 @@ def _on(device, call, made, stream, where, args, others=()):
         if t is not None and t.device != device:
             raise ValueError(f"{name} must be on {device}")
     index = device.index
-    if index == torch.cuda.current_device():
-        return _launch(device, call, made, stream, where, args)
-    with torch.cuda.device(index):
-        return _launch(device, call, made, stream, where, args)
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _launch(index, call, made, stream, where, args)
+    return _launch(index, call, made, stream, where, args)
 
 
-def _launch(device, call, made, stream, where, args):
-    own = torch.cuda.current_stream(device)
-    s = own if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"the stream must belong to {device}")
-    _check(call(*args, s.cuda_stream), where)
-    if s.cuda_stream != own.cuda_stream:
-        for t in made:
-            t.record_stream(s)
+def _launch(index, call, made, stream, where, args):
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or stream.cuda_stream == raw:
+        status = call(*args, raw)
+        if status:
+            raise Q8Error(status, where)
+        return
+    if stream.device_index != index:
+        raise ValueError(f"the stream must belong to cuda:{index}")
+    _check(call(*args, stream.cuda_stream), where)
+    for t in made:
+        t.record_stream(stream)
 
 
 def _check_out(out, shape, dtype, device, name="out"):
@@ -591,9 +597,14 @@ def _check_out(out, shape, dtype, device, name="out"):
     return out
 
 
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _ld(t: torch.Tensor) -> int:
     # The stride of a single row means nothing to torch: the row's length stands for it.
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
 
 
 def _check_bias(bias, n, device):
@@ -650,7 +661,7 @@ def q8_linear_fp8_block(x: QActBlock, w: QWeightBlock, bias: Optional[torch.Tens
         _check_out(out, (cx.m, cw.n), torch.bfloat16, dev)
     _check_bias(bias, cw.n, dev)
     _on(dev, _lib.q8_linear_fp8_block, made, stream, "q8_linear_fp8_block",
-        (ctypes.byref(cx), ctypes.byref(cw), _ptr(bias), out.data_ptr(), _ld(out)), ((w.codes, "w"),))
+        (ctypes.byref(cx), ctypes.byref(cw), _addr(bias), out.data_ptr(), _ld(out)), ((w.codes, "w"),))
     return out
 
 
@@ -674,8 +685,8 @@ def q8_linear_fp8_block_dynamic(X: torch.Tensor, w: QWeightBlock, bias: Optional
         made.append(workspace)
     _check_bias(bias, cw.n, dev)
     _on(dev, _lib.q8_linear_fp8_block_dynamic, made, stream, "q8_linear_fp8_block_dynamic",
-        (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, k, _ld(X), ctypes.byref(cw), _ptr(bias), out.data_ptr(), _ld(out),
-         _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()),
+        (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, k, _ld(X), ctypes.byref(cw), _addr(bias), out.data_ptr(), _ld(out),
+         _addr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()),
         ((w.codes, "w"), (workspace, "workspace")))
     return out
 
@@ -699,7 +710,7 @@ def q8_linear_fp8_block_grouped(x: QActBlock, w: QWeightBlock, offsets: torch.Te
         _check_out(out, (cx.m, n), torch.bfloat16, dev)
     _check_bias(bias, cw.n, dev)
     _on(dev, _lib.q8_linear_fp8_block_grouped, made, stream, "q8_linear_fp8_block_grouped",
-        (ctypes.byref(cx), ctypes.byref(cw), e, offsets.data_ptr(), _ptr(bias), out.data_ptr(), _ld(out)),
+        (ctypes.byref(cx), ctypes.byref(cw), e, offsets.data_ptr(), _addr(bias), out.data_ptr(), _ld(out)),
         ((w.codes, "w"),))
     return out
 
@@ -763,7 +774,7 @@ def q8_moe_fp8_block(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
         made.append(workspace)
     _on(dev, _lib.q8_moe_fp8_block, made, stream, "q8_moe_fp8_block",
         (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, hidden, _ld(X), ids.data_ptr(), weights.data_ptr(), top_k,
-         ctypes.byref(c13), ctypes.byref(c2), experts, out.data_ptr(), _ld(out), _ptr(workspace),
+         ctypes.byref(c13), ctypes.byref(c2), experts, out.data_ptr(), _ld(out), _addr(workspace),
          workspace.numel() * workspace.element_size()),
         ((w13.codes, "w13"), (w2.codes, "w2"), (workspace, "workspace")))
     return out
