@@ -116,7 +116,7 @@ constexpr int64_t kMaxMoeDim = 65536;
 
 // Output tiles of a block-scaled linear are counted in 32 bits.
 bool block_tiles_fit(int64_t m, int64_t n, int64_t experts) {
-    return ((m + 255) / 256 + experts) * blocks128(n) <= kMaxDim;
+    return (blocks128(m) + experts) * blocks128(n) <= kMaxDim;
 }
 
 q8_status check_weight(const q8_weight* w) {

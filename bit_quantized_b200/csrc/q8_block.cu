@@ -127,21 +127,27 @@ weight_block_quant_kernel(const T* __restrict__ W, int64_t n, int64_t k, int64_t
 }
 
 // ============================================================================
-// Pair kernel: 256 x BN tiles on the two SMs of a CTA pair, persistent
+// Tile kernel: 128 x BN output tiles, persistent
 // ============================================================================
 //
-// Roles as in the rowwise pair GEMM (TMA producer, MMA issuer in the even CTA),
-// but eight promotion warps per CTA: a warp reads its 32-lane quarter of TMEM
-// (its threads' token rows) and half of the tile's columns, BN / 2 fp32 sums
-// per thread.  Every K group is handed over through the accumulator barriers,
-// and the sums leave through TMA stores when the tile is done.
+// Roles as in the rowwise tile GEMM (TMA producer, MMA issuer), but eight
+// promotion warps: a warp reads its 32-lane quarter of TMEM (its threads' token
+// rows) and half of the tile's columns, BN / 2 fp32 sums per thread.  Every K
+// group is handed over through the accumulator barriers, and the sums leave
+// through TMA stores when the tile is done.
+//
+// One CTA per tile, not a CTA pair: with two accumulators in TMEM the MMA of
+// group j + 2 waits for the promotion of group j, and across a pair that round
+// trip (commit to both CTAs, arrivals from both) takes about 1400 cycles per two
+// groups of 512 each; inside one CTA it fits under the MMAs, which is worth
+// more than the pair's smaller operand traffic.
 
 constexpr int kPromoWarps = 8;
-constexpr int kPairThreads = 128 + 32 * kPromoWarps;
+constexpr int kTileThreads = 128 + 32 * kPromoWarps;
 // Registers: 384 threads launch with 168 each (64,512); the first warpgroup
 // (TMA, MMA, two idle warps) keeps 72 and the two promotion warpgroups take 216
 // (128 x 72 + 256 x 216 = 64,512), which holds 128 fp32 sums per thread.
-constexpr int kPairRegsLow = 72, kPairRegsHigh = 216;
+constexpr int kTileRegsLow = 72, kTileRegsHigh = 216;
 
 struct BlockParams {
     int m, n;
@@ -154,11 +160,11 @@ struct BlockParams {
 };
 
 template <int BN>
-struct BlockPairCfg {
+struct BlockTileCfg {
     static constexpr int A_BYTES = kBM * kBKB;
-    static constexpr int B_BYTES = (BN / 2) * kBKB;
+    static constexpr int B_BYTES = BN * kBKB;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STORE = kPromoWarps * 2 * 2048;   // output staging: two 32 x 32 chunks per warp
+    static constexpr int STORE = kPromoWarps * 2048;       // output staging: one 32 x 32 chunk per warp
     static constexpr int STAGES_RAW = (227 * 1024 - STORE - 1024 - 6 * 1024) / STAGE;
     static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
     static constexpr int TMEM_COLS = 2 * BN;
@@ -168,11 +174,11 @@ struct BlockPairCfg {
 };
 
 template <int BN, bool GROUPED>
-__global__ void __launch_bounds__(kPairThreads, 1)
-gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+__global__ void __launch_bounds__(kTileThreads, 1)
+gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY, int use_tmy, const BlockParams p, int num_kb,
                        int tiles_m, int tiles_n, const int32_t* group_offsets, int experts) {
-    using C = BlockPairCfg<BN>;
+    using C = BlockTileCfg<BN>;
     __shared__ int g_off[GROUPED ? kMaxGroupedExperts + 1 : 1];
     __shared__ int g_mt[GROUPED ? kMaxGroupedExperts + 1 : 1];
     extern __shared__ uint8_t smem_raw[];
@@ -187,9 +193,6 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
 
     const int warp = warp_index();
     const int lane = threadIdx.x % 32;
-    const uint32_t rank = cluster_ctarank();          // 0: issues the pair's MMAs
-    const int pair = static_cast<int>(blockIdx.x >> 1);
-    const int npairs = static_cast<int>(gridDim.x >> 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -198,52 +201,49 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], 2 * kPromoWarps);
+            mbar_init(&tempty_bar[b], kPromoWarps);
         }
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc_pair(&tmem_base_sh, C::TMEM_COLS);
-        tmem_relinquish_pair();
+        tmem_alloc(&tmem_base_sh, C::TMEM_COLS);
+        tmem_relinquish();
     }
     if constexpr (GROUPED) {
         // The routing offsets come from the previous kernels.
         pdl_wait();
-        if (warp == 2) build_group_map(group_offsets, experts, p.m, 2 * kBM, g_off, g_mt);
+        if (warp == 2) build_group_map(group_offsets, experts, p.m, kBM, g_off, g_mt);
     }
     tc_fence_before();
     __syncthreads();
-    // Both CTAs' barriers are initialized before either touches the other's.
-    cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
     pdl_launch_dependents();
 
     const int num_tiles = GROUPED ? g_mt[GROUPED ? experts : 0] * tiles_n : tiles_m * tiles_n;
+    const int first_tile = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
     auto tile_ref = [&](int tile) -> TileRef {
-        if constexpr (GROUPED) return grouped_tile(tile, g_off, g_mt, experts, 2 * kBM, BN, p.n);
-        else return dense_tile(tile, tiles_m, 2 * kBM, BN, p.m);
+        if constexpr (GROUPED) return grouped_tile(tile, g_off, g_mt, experts, kBM, BN, p.n);
+        else return dense_tile(tile, tiles_m, kBM, BN, p.m);
     };
     if (warp == 0) {
-        reg_dealloc<kPairRegsLow>();
-        // ------------------------------------------------ TMA producer (both CTAs)
+        reg_dealloc<kTileRegsLow>();
+        // ------------------------------------------------ TMA producer
         if (elect_one()) {
             tma_prefetch_desc(&tmA);
             tma_prefetch_desc(&tmB);
-            const uint32_t full0 = map_shared_rank(smem_addr(&full_bar[0]), 0);
             // The weights do not depend on the previous kernel: the first ring
-            // of the first tile's weight halves goes out before the wait.
+            // of the first tile's weight slices goes out before the wait.
             int npre = 0;
             if constexpr (!GROUPED) {
-                if (pair < num_tiles) {
-                    const TileRef tr0 = tile_ref(pair);
+                if (first_tile < num_tiles) {
+                    const TileRef tr0 = tile_ref(first_tile);
                     npre = num_kb < C::STAGES ? num_kb : C::STAGES;
                     for (int s = 0; s < npre; ++s) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], 2 * C::STAGE);
-                        tma_load_2d_pair(smem + s * C::STAGE + C::A_BYTES, &tmB, full0 + 8u * static_cast<uint32_t>(s),
-                                         s * kBKB, tr0.b_row + static_cast<int>(rank) * (BN / 2));
+                        mbar_arrive_expect_tx(&full_bar[s], C::STAGE);
+                        tma_load_2d(smem + s * C::STAGE + C::A_BYTES, &tmB, &full_bar[s], s * kBKB, tr0.b_row);
                     }
                 }
             }
@@ -252,21 +252,18 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+            for (int tile = first_tile; tile < num_tiles && ok; tile += step) {
                 const TileRef tr = tile_ref(tile);
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    const bool pre = tile == pair && kb < npre;   // weight half already out
+                    const bool pre = tile == first_tile && kb < npre;   // weight slice already out
                     if (!pre && !mbar_wait_short(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
                     uint8_t* sa = smem + stage * C::STAGE;
-                    if (rank == 0 && !pre) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE);
-                    const uint32_t fb = full0 + 8u * static_cast<uint32_t>(stage);
-                    tma_load_2d_pair(sa, &tmA, fb, kb * kBKB, tr.a_row + static_cast<int>(rank) * kBM);
-                    if (!pre)
-                        tma_load_2d_pair(sa + C::A_BYTES, &tmB, fb, kb * kBKB,
-                                         tr.b_row + static_cast<int>(rank) * (BN / 2));
+                    if (!pre) mbar_arrive_expect_tx(&full_bar[stage], C::STAGE);
+                    tma_load_2d(sa, &tmA, &full_bar[stage], kb * kBKB, tr.a_row);
+                    if (!pre) tma_load_2d(sa + C::A_BYTES, &tmB, &full_bar[stage], kb * kBKB, tr.b_row);
                     issued |= 1u << stage;
                     last_par = (last_par & ~(1u << stage)) | (phase << stage);
                     if (++stage == C::STAGES) {
@@ -275,77 +272,71 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     }
                 }
             }
-            // Abort: the pair's loads land (on the even CTA's barriers, which
-            // count both CTAs' bytes) before either CTA leaves.
-            if (!ok && rank == 0)
+            if (!ok)   // the loads already issued land before the CTA leaves
                 for (int s = 0; s < C::STAGES; ++s)
                     if (issued & (1u << s)) mbar_wait(&full_bar[s], (last_par >> s) & 1, nullptr, nullptr);
         }
         __syncwarp();
     } else if (warp == 1) {
-        reg_dealloc<kPairRegsLow>();
-        // ------------------------------------------------ MMA issuer (even CTA)
-        if (rank == 0) {
-            // The whole warp runs the loop and one lane issues: descriptors then
-            // stay in uniform registers, without which an MMA takes about 75
-            // cycles to issue and the issue bounds the kernel.
-            const bool leader = elect_one();
-            const uint32_t idesc = make_idesc(1, 0, 0, 2 * kBM, BN);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
-            bool ok = true;
-            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem_base + buf * BN;
-                    const uint32_t sa = smem_addr(smem + stage * C::STAGE);
-                    const uint64_t ad = sdesc_kmajor_sw128(sa);
-                    const uint64_t bd = sdesc_kmajor_sw128(sa + C::A_BYTES);
-                    if (leader) {
-#pragma unroll
-                        for (int ks = 0; ks < kBKB / 32; ++ks)
-                            mma_issue_pair<kKindF8>(d, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-                        tc_commit_pair(&tfull_bar[buf], 0x3);
-                        tc_commit_pair(&empty_bar[stage], 0x3);
-                    }
-                    __syncwarp();
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                    buf ^= 1;
-                    if (buf == 0) bphase ^= 1;
+        reg_dealloc<kTileRegsLow>();
+        // ------------------------------------------------ MMA issuer
+        // The whole warp runs the loop and one lane issues: descriptors then
+        // stay in uniform registers, without which an MMA takes about 75 cycles
+        // to issue and the issue bounds the kernel.
+        const bool leader = elect_one();
+        const uint32_t idesc = make_idesc(1, 0, 0, kBM, BN);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+        for (int tile = first_tile; tile < num_tiles && ok; tile += step) {
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status) ||
+                    !mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status)) {
+                    ok = false;
+                    break;
                 }
+                tc_fence_after();
+                const uint32_t d = tmem_base + buf * BN;
+                const uint32_t sa = smem_addr(smem + stage * C::STAGE);
+                const uint64_t ad = sdesc_kmajor_sw128(sa);
+                const uint64_t bd = sdesc_kmajor_sw128(sa + C::A_BYTES);
+                if (leader) {
+#pragma unroll
+                    for (int ks = 0; ks < kBKB / 32; ++ks)
+                        mma_issue<kKindF8>(d, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                    tc_commit(&tfull_bar[buf]);
+                    tc_commit(&empty_bar[stage]);
+                }
+                __syncwarp();
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1;
             }
-            if (!ok && leader) {
-                // Abort: wait for the MMAs already issued before TMEM is freed.
-                tc_commit_pair_local(&drain_bar);
-                mbar_wait(&drain_bar, 0, nullptr, nullptr);
-            }
+        }
+        if (!ok && leader) {
+            // Abort: wait for the MMAs already issued before TMEM is freed.
+            tc_commit(&drain_bar);
+            mbar_wait(&drain_bar, 0, nullptr, nullptr);
         }
         __syncwarp();
     } else if (warp < 4) {
-        reg_dealloc<kPairRegsLow>();
+        reg_dealloc<kTileRegsLow>();
     } else {
-        reg_alloc<kPairRegsHigh>();
-        // ------------------------------------------------ promotion and epilogue (both CTAs)
+        reg_alloc<kTileRegsHigh>();
+        // ------------------------------------------------ promotion and epilogue
         pdl_wait();
         const int q = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tempty0 = map_shared_rank(smem_addr(&tempty_bar[0]), 0);
-        uint8_t* store = smem + C::STAGES * C::STAGE + (warp - 4) * 4096;
-        uint32_t sbuf = 0;
+        uint8_t* store = smem + C::STAGES * C::STAGE + (warp - 4) * 2048;
         const int nb_all = (p.n + kBlock - 1) / kBlock;
         int buf = 0;
         uint32_t bphase = 0;
         bool ok = true;
-        for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+        for (int tile = first_tile; tile < num_tiles && ok; tile += step) {
             const TileRef tr = tile_ref(tile);
-            const int row0 = tr.a_row + static_cast<int>(rank) * kBM + q * 32;
+            const int row0 = tr.a_row + q * 32;
             const int row = row0 + lane;
             const int ncol = tr.n_tile + half * C::CW;         // this warp's first column
             int nb = ncol / kBlock;
@@ -360,28 +351,28 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             // volatile and the products are formed at the use: left to itself,
             // the compiler forms them right behind the loads, and every fourth
             // group then waits about 2000 cycles for memory.
-            float a_cur[4], b_cur[4];
-            auto fetch = [&](int kb, float& a, float& b) {
-                const int k = kb < num_kb ? kb : num_kb - 1;   // past the end: loaded, not used
-                a = ldg_volatile(sx + static_cast<int64_t>(k) * p.m);
-                b = ldg_volatile(sw + k);
-            };
+            float s_a[4], s_b[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) fetch(j, a_cur[j], b_cur[j]);
+            for (int j = 0; j < 4; ++j) {
+                s_a[j] = ldg_volatile(sx);
+                s_b[j] = ldg_volatile(sw);
+                if (j + 1 < num_kb) {              // past the end: loaded again, not used
+                    sx += p.m;
+                    ++sw;
+                }
+            }
             for (int kb0 = 0; kb0 < num_kb && ok; kb0 += 4) {
-                float a_nxt[4], b_nxt[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) fetch(kb0 + 4 + j, a_nxt[j], b_nxt[j]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (kb0 + j >= num_kb) break;
+                    const int kb = kb0 + j;
+                    if (kb >= num_kb) break;
                     if (!mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
                     __syncwarp();
                     tc_fence_after();
-                    const float sc = a_cur[j] * b_cur[j];
+                    const float sc = s_a[j] * s_b[j];
                     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * C::CW;
 #pragma unroll
                     for (int c = 0; c < C::CW / 32; ++c) {
@@ -392,17 +383,18 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                             // All of this warp's part is in registers: the buffer may be written again.
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster_no_fence(tempty0 + 8u * static_cast<uint32_t>(buf));
+                            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
                         }
                         promote(acc + c * 16, r, sc);
                     }
+                    s_a[j] = ldg_volatile(sx);
+                    s_b[j] = ldg_volatile(sw);
+                    if (kb + 5 < num_kb) {
+                        sx += p.m;
+                        ++sw;
+                    }
                     buf ^= 1;
                     if (buf == 0) bphase ^= 1;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a_cur[j] = a_nxt[j];
-                    b_cur[j] = b_nxt[j];
                 }
             }
             if (!ok) break;
@@ -433,8 +425,8 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     }
                 }
                 if (tma) {
-                    uint8_t* b = store + sbuf * 2048;
-                    if (lane == 0) bulk_wait_read<1>();        // the buffer's previous store has read it
+                    uint8_t* b = store;
+                    if (lane == 0) bulk_wait_read<0>();        // the previous store has read it
                     __syncwarp();
                     const uint32_t sz = static_cast<uint32_t>((lane >> 1) & 3);   // TMA's 64-byte swizzle
 #pragma unroll
@@ -448,7 +440,6 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                         tma_store_2d(&tmY, b, n0, row0);
                         bulk_commit();
                     }
-                    sbuf ^= 1u;
                 } else if (row < tr.row_end) {
                     uint4* yp = reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(row) * p.ldy + n0);
 #pragma unroll
@@ -465,12 +456,9 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
     }
 
     __syncthreads();
-    // No CTA leaves while its partner may still signal one of its barriers or
-    // read its shared memory.
-    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
 }
 
@@ -835,38 +823,33 @@ BlockParams block_params(const BlockLinearArgs& a) {
 }
 
 template <int BN, bool GROUPED>
-q8_status run_block_pair(const BlockLinearArgs& a, cudaStream_t s) {
-    using C = BlockPairCfg<BN>;
+q8_status run_block_tile(const BlockLinearArgs& a, cudaStream_t s) {
+    using C = BlockTileCfg<BN>;
     CUtensorMap tA, tB, tY;
     if (!make_map(&tA, a.x_codes, false, a.k, a.m, a.ldx, kBKB, kBM) ||
-        !make_map(&tB, a.w_codes, false, a.k, a.experts * a.n, a.ldw, kBKB, BN / 2))
+        !make_map(&tB, a.w_codes, false, a.k, a.experts * a.n, a.ldw, kBKB, BN))
         return Q8_ERR_CUDA;
     const int use_tmy = make_map_y(&tY, a.y, a.n, a.m, a.ldy) ? 1 : 0;
     if (!use_tmy) tY = tA;
-    auto kern = gemm_block_pair_kernel<BN, GROUPED>;
+    auto kern = gemm_block_tile_kernel<BN, GROUPED>;
     if (set_smem(kern, C::SMEM) != cudaSuccess) return Q8_ERR_LAUNCH;
     const int tiles_n = static_cast<int>((a.n + BN - 1) / BN);
-    const int tiles_m = static_cast<int>((a.m + 2 * kBM - 1) / (2 * kBM));
+    const int tiles_m = static_cast<int>((a.m + kBM - 1) / kBM);
     // Grouped: an upper bound (each expert adds at most one partial row tile);
     // the kernel reads the offsets and walks the actual tiles.
     const int64_t tiles = (tiles_m + (GROUPED ? a.experts : 0)) * tiles_n;
-    const int pairs_max = max_pairs(kern, C::SMEM, kPairThreads);
-    const int pairs = static_cast<int>(tiles < pairs_max ? tiles : pairs_max);
+    const int sms = sm_count();
     const int num_kb = static_cast<int>((a.k + kBKB - 1) / kBKB);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles < sms ? tiles : sms), 1, 1);
+    cfg.blockDim = dim3(kTileThreads, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tA, tB, tY, use_tmy, block_params(a), num_kb, tiles_m, tiles_n, a.offsets,
                            static_cast<int>(a.experts)) != cudaSuccess) {
         cudaGetLastError();
@@ -927,13 +910,13 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
     return Q8_OK;
 }
 
-// Tile width of the pair kernel: the persistent grid's makespan, waves x (BN +
-// a tile's fixed cost of about 64 columns' worth), the wider tile on ties.
+// Tile width: the persistent grid's makespan, waves x (BN + a tile's fixed cost
+// of about 64 columns' worth), the wider tile on ties.
 bool wide_tiles(int64_t row_tiles, int64_t n) {
-    const int64_t pairs = sm_count() / 2;
+    const int64_t sms = sm_count();
     auto cost = [&](int64_t bn) {
         const int64_t tiles = row_tiles * ((n + bn - 1) / bn);
-        return ((tiles + pairs - 1) / pairs) * (bn + 64);
+        return ((tiles + sms - 1) / sms) * (bn + 64);
     };
     return cost(256) <= cost(128);
 }
@@ -950,8 +933,8 @@ cudaError_t launch_block_quant(const BlockQuantArgs& a, bool weight, cudaStream_
 
 q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     if (a.offsets) {
-        const int64_t rows = (a.m + 2 * kBM - 1) / (2 * kBM) + a.experts / 2;
-        return wide_tiles(rows, a.n) ? run_block_pair<256, true>(a, s) : run_block_pair<128, true>(a, s);
+        const int64_t rows = (a.m + kBM - 1) / kBM + a.experts / 2;
+        return wide_tiles(rows, a.n) ? run_block_tile<256, true>(a, s) : run_block_tile<128, true>(a, s);
     }
     if (a.x) {   // quantized on the way
         switch (a.x_dtype) {
@@ -964,8 +947,7 @@ q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     if (a.m <= 32) return run_block_decode<32, false, __half>(a, s);
     if (a.m <= 64) return run_block_decode<64, false, __half>(a, s);
     if (a.m <= 2 * kBM) return run_block_decode<128, false, __half>(a, s);
-    return wide_tiles((a.m + 2 * kBM - 1) / (2 * kBM), a.n) ? run_block_pair<256, false>(a, s)
-                                                            : run_block_pair<128, false>(a, s);
+    return wide_tiles((a.m + kBM - 1) / kBM, a.n) ? run_block_tile<256, false>(a, s) : run_block_tile<128, false>(a, s);
 }
 
 }  // namespace q8

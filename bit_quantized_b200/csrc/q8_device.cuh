@@ -364,12 +364,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
                  : "memory");
 }
 
-// The same without a fence at cluster scope, which costs about a thousand
-// cycles: for arrivals that only say that this thread's tensor-memory reads
-// are over (completed by tcgen05.wait::ld) and publish no memory.
-__device__ __forceinline__ void mbar_arrive_cluster_no_fence(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
 
 // ---------------------------------------------------------------- clusters
 
