@@ -136,10 +136,11 @@ struct MoeParams {
     int m, top_k, experts, hidden, inter;
     int rows_max;            // m * top_k
     int it, ht, kb1, kb2;    // 128-wide tiles of inter and hidden; K groups of both products (kb1 = ht, kb2 = it)
-    int* head;               // [0] active experts, [1] rows
-    int* expert; int* base;
-    unsigned long long* mask;
-    int* row_token; float* row_weight;
+    int* head;               // [0] active experts
+    int* expert;             // [active] expert of each active index, ascending
+    int* base;               // [active + 1] first row of its tokens; a row is a (token, expert) pair
+    int* row_token;          // [rows] an expert's tokens, ascending
+    float* row_weight;       // [rows]
     int* up_count; int* down_count;
     uint8_t* xq; float* xs;  // m x hidden codes, [kb1][m]
     uint8_t* hq; float* hs;  // rows x inter codes, [kb2][rows_max]
@@ -222,14 +223,13 @@ moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restri
     const int na = active_sh;
     if (threadIdx.x == 0) {
         p.head[0] = na;
-        p.head[1] = rows_sh;
+        p.base[na] = rows_sh;
     }
     for (int a = threadIdx.x; a < na; a += 256) {
         const int e = list_sh[a];
         const unsigned long long mk = mask_sh[e];
         p.expert[a] = e;
         p.base[a] = base_sh[a];
-        p.mask[a] = mk;
         int r = base_sh[a];
         for (unsigned long long b = mk; b; b &= b - 1) {
             const int t = __ffsll(static_cast<long long>(b)) - 1;
@@ -264,6 +264,19 @@ struct Line {
     }
 };
 
+// The expert list in shared memory, copied by the whole block.
+struct ListSh {
+    int expert[kMaxExperts];
+    int base[kMaxExperts + 1];
+};
+
+__device__ __forceinline__ void copy_list(ListSh& l, const MoeParams& p, int active) {
+    for (int a = threadIdx.x; a <= active; a += blockDim.x) {
+        if (a < active) l.expert[a] = __ldcg(p.expert + a);
+        l.base[a] = active > 0 ? __ldcg(p.base + a) : 0;
+    }
+}
+
 // Counts this CTA's arrival at a tile with `parts` contributors; true in the
 // one that arrives last, which then sees every contributor's sums.  Called by
 // the `threads` threads of the promotion warps, after each wrote its sums.
@@ -288,7 +301,9 @@ struct MoeUpCfg {
     static constexpr int CW = NT / HALVES;            // token columns per promotion warp
     static constexpr int B_BYTES = NT * kBKB;
     static constexpr int STAGE = 2 * kBM * kBKB + B_BYTES;
-    static constexpr int STAGES = (200 * 1024) / STAGE;
+    // Up to 32 tokens two CTAs fit an SM, so that the down projection's can
+    // take their place and ask for their weights while this kernel ends.
+    static constexpr int STAGES = (NT <= 32 ? 103 * 1024 : 200 * 1024) / STAGE;
     static constexpr int TMEM_COLS = 4 * NT;
     static constexpr int SMEM = STAGES * STAGE + 1024;
 };
@@ -308,6 +323,8 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     __shared__ int abort_sh, last_sh;
     __shared__ __align__(16) float col_s[C::PROMO][2][C::CW];
     __shared__ float amax_sh[C::HALVES][4][C::CW];
+    __shared__ ListSh list;
+    __shared__ uint8_t token_sh[kMaxTokens * kMoeMaxTopK];
 
     const int warp = warp_index(), lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -336,7 +353,12 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     // complete here, before it waits for this kernel.
     pdl_launch_dependents();
 
-    const int active = p.head[0];
+    const int active = __ldcg(p.head);
+    copy_list(list, p, active);
+    __syncthreads();
+    const int rows = list.base[active];
+    for (int r = threadIdx.x; r < rows; r += C::THREADS) token_sh[r] = static_cast<uint8_t>(__ldcg(p.row_token + r));
+    __syncthreads();
     const Line line(static_cast<long long>(active) * p.it * p.kb1);
     const int cta = static_cast<int>(blockIdx.x);
     const int s_begin = active > 0 && cta < line.ctas ? line.start(cta) : 0;
@@ -354,17 +376,25 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const int u = s / p.kb1, k0 = s - u * p.kb1;
                 const int k1 = min(p.kb1, k0 + s_end - s);
                 const int a = u / p.it;
-                const int row = p.expert[a] * 2 * p.inter + (u - a * p.it) * kBM;
+                const int row = list.expert[a] * 2 * p.inter + (u - a * p.it) * kBM;
+                const int base = list.base[a], cnt = list.base[a + 1] - base;
+                const int quads = (cnt + 3) / 4;
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_short(&empty_bar[stage], phase ^ 1, &abort_sh, p.status)) {
                         ok = false;
                         break;
                     }
                     uint8_t* sa = smem + stage * C::STAGE;
-                    mbar_arrive_expect_tx(&full_bar[stage], C::STAGE);
+                    mbar_arrive_expect_tx(&full_bar[stage], 2 * kBM * kBKB + quads * 4 * kBKB);
                     tma_load_2d(sa, &tmW, &full_bar[stage], kb * kBKB, row);
                     tma_load_2d(sa + kBM * kBKB, &tmW, &full_bar[stage], kb * kBKB, row + p.inter);
-                    tma_load_2d(sa + 2 * kBM * kBKB, &tmX, &full_bar[stage], kb * kBKB, 0);
+                    // The expert's tokens, four rows of x at a time (the last one again past the end).
+                    for (int b = 0; b < quads; ++b) {
+                        const uint8_t* tk = token_sh + base + 4 * b;
+                        const int last = cnt - 1 - 4 * b;
+                        tma_gather4(sa + (2 * kBM + 4 * b) * kBKB, &tmX, &full_bar[stage], kb * kBKB, tk[0],
+                                    tk[min(1, last)], tk[min(2, last)], tk[min(3, last)]);
+                    }
                     issued |= 1u << stage;
                     last_par = (last_par & ~(1u << stage)) | (phase << stage);
                     if (++stage == C::STAGES) {
@@ -384,37 +414,44 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             // The whole warp runs the loop and one lane issues: descriptors then
             // stay in uniform registers.
             const bool leader = elect_one();
-            const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((p.m + 15) / 16 * 16));
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
-            for (int s = s_begin; s < s_end; ++s) {
-                if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                    !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t sa = smem_addr(smem + stage * C::STAGE);
-                const uint64_t gd = sdesc_kmajor_sw128(sa), ud = sdesc_kmajor_sw128(sa + kBM * kBKB);
-                const uint64_t bd = sdesc_kmajor_sw128(sa + 2 * kBM * kBKB);
-                const uint32_t d = tmem_base + buf * 2 * NT;
-                if (leader) {
-#pragma unroll
-                    for (int ks = 0; ks < kBKB / 32; ++ks) {
-                        mma_issue<kKindF8>(d, gd + 2 * ks, bd + 2 * ks, idesc, ks != 0);
-                        mma_issue<kKindF8>(d + NT, ud + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+            for (int s = s_begin; s < s_end && ok;) {
+                const int u = s / p.kb1, k0 = s - u * p.kb1;
+                const int k1 = min(p.kb1, k0 + s_end - s);
+                const int a = u / p.it;
+                const int cnt = list.base[a + 1] - list.base[a];
+                const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
+                        ok = false;
+                        break;
                     }
-                    tc_commit(&tfull_bar[buf]);
-                    tc_commit(&empty_bar[stage]);
+                    tc_fence_after();
+                    const uint32_t sa = smem_addr(smem + stage * C::STAGE);
+                    const uint64_t gd = sdesc_kmajor_sw128(sa), ud = sdesc_kmajor_sw128(sa + kBM * kBKB);
+                    const uint64_t bd = sdesc_kmajor_sw128(sa + 2 * kBM * kBKB);
+                    const uint32_t d = tmem_base + buf * 2 * NT;
+                    if (leader) {
+#pragma unroll
+                        for (int ks = 0; ks < kBKB / 32; ++ks) {
+                            mma_issue<kKindF8>(d, gd + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                            mma_issue<kKindF8>(d + NT, ud + 2 * ks, bd + 2 * ks, idesc, ks != 0);
+                        }
+                        tc_commit(&tfull_bar[buf]);
+                        tc_commit(&empty_bar[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    buf ^= 1;
+                    if (buf == 0) bphase ^= 1;
                 }
-                __syncwarp();
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                buf ^= 1;
-                if (buf == 0) bphase ^= 1;
+                s += k1 - k0;
             }
             if (!ok && leader) {
                 tc_commit(&drain_bar);
@@ -436,16 +473,15 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             const int u = s / p.kb1, k0 = s - u * p.kb1;
             const int k1 = min(p.kb1, k0 + s_end - s);
             const int a = u / p.it, it = u - a * p.it;
-            const int e = p.expert[a];
-            // this warp's columns that the expert's tokens fill
-            const uint32_t want = static_cast<uint32_t>((p.mask[a] >> c0) & ((1ull << C::CW) - 1ull));
+            const int e = list.expert[a], row0 = list.base[a] + c0;   // this warp's columns are rows row0 ..
+            const int cn = min(C::CW, list.base[a + 1] - row0);       // and how many it has (may be none)
             const float* sg = p.s13 + (static_cast<int64_t>(e) * 2 * p.it + it) * p.kb1;
             const float* su = sg + static_cast<int64_t>(p.it) * p.kb1;
             float2 g[C::CW / 2], w[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
-            const int t = c0 + lane;                        // CW <= 32: one column scale per lane
-            const bool have = lane < C::CW && t < p.m;
+            const bool have = lane < cn;                    // CW <= 32: one column scale per lane
+            const int t = have ? token_sh[row0 + lane] : 0;
             float sx = have ? __ldcg(p.xs + static_cast<int64_t>(k0) * p.m + t) : 0.f;
             float wg = __ldg(sg + k0), wu = __ldg(su + k0);
             for (int kb = k0; kb < k1; ++kb) {
@@ -466,7 +502,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 2 * NT + c0;
 #pragma unroll
                 for (int c = 0; c < C::CW / 16; ++c) {
-                    if ((want >> (c * 16)) & 0xFFFFu) {
+                    if (c * 16 < cn) {
                         uint32_t rg[16], ru[16];
                         tmem_ld16(tb + c * 16, rg);
                         tmem_ld16(tb + NT + c * 16, ru);
@@ -487,7 +523,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 float* mine = p.part + (static_cast<int64_t>(cta) * 2 + (k0 > 0 ? 0 : 1)) * (2 * NT * kBM) + ch;
 #pragma unroll
                 for (int i = 0; i < C::CW; ++i) {
-                    if ((want >> i) & 1u) {
+                    if (i < cn) {
                         mine[(c0 + i) * kBM] = (i & 1) ? g[i / 2].y : g[i / 2].x;
                         mine[(NT + c0 + i) * kBM] = (i & 1) ? w[i / 2].y : w[i / 2].x;
                     }
@@ -499,28 +535,28 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
                     for (int c = first; c <= lastc; ++c) {
                         const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
+                        // All of a contributor's sums are asked for before any is added.
+                        float x[C::CW], v[C::CW];
 #pragma unroll
                         for (int i = 0; i < C::CW; ++i) {
-                            if ((want >> i) & 1u) {
-                                const float x = __ldcg(src + (c0 + i) * kBM), v = __ldcg(src + (NT + c0 + i) * kBM);
-                                if (i & 1) {
-                                    g[i / 2].y += x;
-                                    w[i / 2].y += v;
-                                } else {
-                                    g[i / 2].x += x;
-                                    w[i / 2].x += v;
-                                }
-                            }
+                            x[i] = i < cn ? __ldcg(src + (c0 + i) * kBM) : 0.f;
+                            v[i] = i < cn ? __ldcg(src + (NT + c0 + i) * kBM) : 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < C::CW / 2; ++i) {
+                            g[i].x += x[2 * i];
+                            g[i].y += x[2 * i + 1];
+                            w[i].x += v[2 * i];
+                            w[i].y += v[2 * i + 1];
                         }
                     }
                 }
             }
             if (finish) {
                 // h = silu(G) U of this tile: one scale group of h per token.
-                const int rbase = p.base[a] + __popcll(p.mask[a] & ((1ull << c0) - 1ull));
 #pragma unroll
                 for (int i = 0; i < C::CW; ++i) {
-                    if ((want >> i) & 1u) {
+                    if (i < cn) {
                         float& gi = (i & 1) ? g[i / 2].y : g[i / 2].x;
                         const float ui = (i & 1) ? w[i / 2].y : w[i / 2].x;
                         gi = gi / (1.0f + expf(-gi)) * ui;
@@ -531,8 +567,8 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 named_barrier(2 + half, 128);
 #pragma unroll
                 for (int i = 0; i < C::CW; ++i) {
-                    if ((want >> i) & 1u) {
-                        const int r = rbase + __popc(want & ((1u << i) - 1u));
+                    if (i < cn) {
+                        const int r = row0 + i;
                         const float am = fmaxf(fmaxf(amax_sh[half][0][i], amax_sh[half][1][i]),
                                                fmaxf(amax_sh[half][2][i], amax_sh[half][3][i]));
                         const BlockScale bs = block_scale(am);
@@ -561,7 +597,7 @@ struct MoeDownCfg {
     static constexpr int B_BYTES = NT * kBKB;
     static constexpr int STAGE = kBM * kBKB + B_BYTES;
     static constexpr int OUT = NT * kBM * 4;          // the tile's sums over experts
-    static constexpr int STAGES_RAW = (200 * 1024 - OUT) / STAGE;
+    static constexpr int STAGES_RAW = ((NT <= 32 ? 103 * 1024 : 200 * 1024) - OUT) / STAGE;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
     static constexpr int TMEM_COLS = 2 * NT;
     static constexpr int SMEM = STAGES * STAGE + OUT + 1024;
@@ -582,6 +618,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, last_sh;
     __shared__ __align__(16) float col_s[4][NT];
+    __shared__ ListSh list;
 
     const int warp = warp_index(), lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -609,6 +646,8 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 
     // The expert list was complete before the up projection let this kernel start.
     const int active = __ldcg(p.head);
+    copy_list(list, p, active);
+    __syncthreads();
     const int tile_steps = active * p.kb2;           // of one output tile
     const Line line(static_cast<long long>(tile_steps) * p.ht);
     const int cta = static_cast<int>(blockIdx.x);
@@ -633,9 +672,9 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     const int v = s / p.kb2, k0 = s - v * p.kb2;
                     const int k1 = min(p.kb2, k0 + end - s);
                     const int nt = v / active, a = v - nt * active;
-                    const int row = __ldcg(p.expert + a) * p.hidden + nt * kBM;
-                    const int base = __ldcg(p.base + a);
-                    const int boxes = (__popcll(__ldcg(p.mask + a)) + 15) / 16;
+                    const int row = list.expert[a] * p.hidden + nt * kBM;
+                    const int base = list.base[a];
+                    const int boxes = (list.base[a + 1] - base + 15) / 16;
                     for (int kb = k0; kb < k1; ++kb, ++s) {
                         const bool early = s - s_begin < first;
                         uint8_t* sa = smem + stage * C::STAGE;
@@ -673,7 +712,8 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             for (int s = s_begin; s < s_end && ok;) {
                 const int v = s / p.kb2, k0 = s - v * p.kb2;
                 const int k1 = min(p.kb2, k0 + s_end - s);
-                const int cnt = __popcll(__ldcg(p.mask + v % active));
+                const int a = v % active;
+                const int cnt = list.base[a + 1] - list.base[a];
                 const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
@@ -731,8 +771,8 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 const int v = s / p.kb2, k0 = s - v * p.kb2;
                 const int k1 = min(p.kb2, k0 + s1 - s);
                 const int a = v - nt * active;
-                const int e = __ldcg(p.expert + a), base = __ldcg(p.base + a);
-                const int cnt = __popcll(__ldcg(p.mask + a));
+                const int e = list.expert[a], base = list.base[a];
+                const int cnt = list.base[a + 1] - base;
                 const float* sw = p.s2 + (static_cast<int64_t>(e) * p.ht + nt) * p.kb2;
                 float2 acc[NT / 2];
 #pragma unroll
@@ -747,6 +787,14 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     }
                 };
                 fetch(k0);
+                int tk[NS];                      // the rows' tokens and weights, one row per lane
+                float wt[NS];
+#pragma unroll
+                for (int c = 0; c < NS; ++c) {
+                    const bool have = c * 32 + lane < cnt;
+                    tk[c] = have ? __ldcg(p.row_token + base + c * 32 + lane) : 0;
+                    wt[c] = have ? __ldcg(p.row_weight + base + c * 32 + lane) : 0.f;
+                }
                 for (int kb = k0; kb < k1; ++kb) {
                     __syncwarp();
 #pragma unroll
@@ -780,9 +828,9 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     if (i < cnt) {
-                        const int t = __ldcg(p.row_token + base + i);
-                        const float wt = __ldcg(p.row_weight + base + i);
-                        oc[t * kBM] = __fmaf_rn(wt, (i & 1) ? acc[i / 2].y : acc[i / 2].x, oc[t * kBM]);
+                        const int t = __shfl_sync(0xffffffffu, tk[i / 32], i % 32);
+                        const float wi = __shfl_sync(0xffffffffu, wt[i / 32], i % 32);
+                        oc[t * kBM] = __fmaf_rn(wi, (i & 1) ? acc[i / 2].y : acc[i / 2].x, oc[t * kBM]);
                     }
                 }
                 s += k1 - k0;
@@ -796,10 +844,13 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 lastc = line.owner(tile1 - 1);
                 finish = arrive_last(&p.down_count[nt], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1, 128);
                 if (finish) {
-                    for (int t = 0; t < p.m; ++t) oc[t * kBM] = 0.f;
-                    for (int c = first; c <= lastc; ++c) {
-                        const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) + ch;
-                        for (int t = 0; t < p.m; ++t) oc[t * kBM] += __ldcg(src + t * kBM);
+                    for (int t = 0; t < p.m; ++t) {
+                        float sum = 0.f;
+#pragma unroll 4
+                        for (int c = first; c <= lastc; ++c)
+                            sum += __ldcg(p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) +
+                                          t * kBM + ch);
+                        oc[t * kBM] = sum;
                     }
                 }
             }
@@ -849,8 +900,7 @@ int64_t layout(const MoeLayerArgs& a, uint8_t* base, MoeParams* p) {
     };
     uint8_t* head = take(8);
     uint8_t* expert = take(4 * act);
-    uint8_t* first = take(4 * act);
-    uint8_t* mask = take(8 * act);
+    uint8_t* first = take(4 * (act + 1));
     uint8_t* token = take(4 * rows);
     uint8_t* weight = take(4 * rows);
     uint8_t* upc = take(4 * act * it);
@@ -874,7 +924,6 @@ int64_t layout(const MoeLayerArgs& a, uint8_t* base, MoeParams* p) {
         p->head = reinterpret_cast<int*>(head);
         p->expert = reinterpret_cast<int*>(expert);
         p->base = reinterpret_cast<int*>(first);
-        p->mask = reinterpret_cast<unsigned long long*>(mask);
         p->row_token = reinterpret_cast<int*>(token);
         p->row_weight = reinterpret_cast<float*>(weight);
         p->up_count = reinterpret_cast<int*>(upc);
@@ -923,7 +972,7 @@ template <int NT>
 q8_status products(const MoeLayerArgs& a, const MoeParams& p, cudaStream_t s) {
     CUtensorMap tW13, tX, tW2, tH;
     if (!make_map(&tW13, a.w13, false, a.hidden, a.experts * 2 * a.inter, a.ld13, kBKB, kBM) ||
-        !make_map(&tX, p.xq, false, a.hidden, a.m, a.hidden, kBKB, NT) ||
+        !make_map(&tX, p.xq, false, a.hidden, a.m, a.hidden, kBKB, 1) ||
         !make_map(&tW2, a.w2, false, a.inter, a.experts * a.hidden, a.ld2, kBKB, kBM) ||
         !make_map(&tH, p.hq, false, a.inter, p.rows_max, a.inter, kBKB, 16))
         return Q8_ERR_CUDA;
