@@ -277,6 +277,11 @@ __device__ __forceinline__ void copy_list(ListSh& l, const MoeParams& p, int act
     }
 }
 
+// The scales of a step are asked for kAhead steps before their use, across tile
+// and expert borders, by asynchronous copies into a ring of each promotion warp
+// (a weight's scale comes from memory, and a step is only a few hundred cycles).
+constexpr int kAhead = 6, kScaleRing = 8;
+
 // Counts this CTA's arrival at a tile with `parts` contributors; true in the
 // one that arrives last, which then sees every contributor's sums.  Called by
 // the `threads` threads of the promotion warps, after each wrote its sums.
@@ -303,7 +308,7 @@ struct MoeUpCfg {
     static constexpr int STAGE = 2 * kBM * kBKB + B_BYTES;
     // Up to 32 tokens two CTAs fit an SM, so that the down projection's can
     // take their place and ask for their weights while this kernel ends.
-    static constexpr int STAGES = (NT <= 32 ? 103 * 1024 : 200 * 1024) / STAGE;
+    static constexpr int STAGES = NT <= 32 ? 3 : 5;
     static constexpr int TMEM_COLS = 4 * NT;
     static constexpr int SMEM = STAGES * STAGE + 1024;
 };
@@ -323,6 +328,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     __shared__ int abort_sh, last_sh;
     __shared__ __align__(16) float col_s[C::PROMO][2][C::CW];
     __shared__ float amax_sh[C::HALVES][4][C::CW];
+    __shared__ float sx_ring[C::PROMO][kScaleRing][C::CW], sw_ring[C::PROMO][kScaleRing][2];
     __shared__ ListSh list;
     __shared__ uint8_t token_sh[kMaxTokens * kMoeMaxTopK];
 
@@ -464,6 +470,40 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         const int ch = q * 32 + lane;
         const int c0 = half * C::CW;
         float* cs = &col_s[warp - 2][0][0];
+        // The step whose scales are asked for next.
+        int as = s_begin, akb = 0, ait = 0, aa = -1, acn = 0, atok = 0;
+        const float* asw = nullptr;
+        if (s_begin < s_end) {
+            const int u0 = s_begin / p.kb1;
+            akb = s_begin - u0 * p.kb1;
+            aa = u0 / p.it;
+            ait = u0 - aa * p.it;
+        }
+        auto enter = [&] {                                  // its tile
+            const int row0 = list.base[aa] + c0;
+            acn = min(C::CW, list.base[aa + 1] - row0);
+            atok = lane < acn ? token_sh[row0 + lane] : 0;
+            asw = p.s13 + (static_cast<int64_t>(list.expert[aa]) * 2 * p.it + ait) * p.kb1;
+        };
+        auto ask = [&] {
+            if (as < s_end) {
+                const int slot = (as - s_begin) % kScaleRing;
+                if (lane < acn) cp_async4(&sx_ring[warp - 2][slot][lane], p.xs + static_cast<int64_t>(akb) * p.m + atok);
+                if (lane < 2) cp_async4(&sw_ring[warp - 2][slot][lane], asw + static_cast<int64_t>(lane) * p.it * p.kb1 + akb);
+                ++as;
+                if (++akb == p.kb1) {
+                    akb = 0;
+                    if (++ait == p.it) {
+                        ait = 0;
+                        ++aa;
+                    }
+                    if (as < s_end) enter();
+                }
+            }
+            cp_async_commit();
+        };
+        if (s_begin < s_end) enter();
+        for (int i = 0; i < kAhead; ++i) ask();
         int buf = 0;
         uint32_t bphase = 0;
         // After a wait that ran out, the warps stop waiting and reading TMEM but
@@ -473,27 +513,20 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             const int u = s / p.kb1, k0 = s - u * p.kb1;
             const int k1 = min(p.kb1, k0 + s_end - s);
             const int a = u / p.it, it = u - a * p.it;
-            const int e = list.expert[a], row0 = list.base[a] + c0;   // this warp's columns are rows row0 ..
-            const int cn = min(C::CW, list.base[a + 1] - row0);       // and how many it has (may be none)
-            const float* sg = p.s13 + (static_cast<int64_t>(e) * 2 * p.it + it) * p.kb1;
-            const float* su = sg + static_cast<int64_t>(p.it) * p.kb1;
+            const int row0 = list.base[a] + c0;             // this warp's columns are rows row0 ..
+            const int cn = min(C::CW, list.base[a + 1] - row0);   // and how many it has (may be none)
             float2 g[C::CW / 2], w[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
-            const bool have = lane < cn;                    // CW <= 32: one column scale per lane
-            const int t = have ? token_sh[row0 + lane] : 0;
-            float sx = have ? __ldcg(p.xs + static_cast<int64_t>(k0) * p.m + t) : 0.f;
-            float wg = __ldg(sg + k0), wu = __ldg(su + k0);
             for (int kb = k0; kb < k1; ++kb) {
+                ask();
+                cp_async_wait<kAhead>();
                 __syncwarp();
+                const int slot = (s + kb - k0 - s_begin) % kScaleRing;
                 if (lane < C::CW) {
-                    cs[lane] = sx * wg;
-                    cs[C::CW + lane] = sx * wu;
-                }
-                if (kb + 1 < k1) {
-                    sx = have ? __ldcg(p.xs + static_cast<int64_t>(kb + 1) * p.m + t) : 0.f;
-                    wg = __ldg(sg + kb + 1);
-                    wu = __ldg(su + kb + 1);
+                    const float sx = sx_ring[warp - 2][slot][lane];
+                    cs[lane] = sx * sw_ring[warp - 2][slot][0];
+                    cs[C::CW + lane] = sx * sw_ring[warp - 2][slot][1];
                 }
                 ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
                 ok = __all_sync(0xffffffffu, ok);
@@ -600,6 +633,7 @@ struct MoeDownCfg {
     static constexpr int STAGES_RAW = ((NT <= 32 ? 103 * 1024 : 200 * 1024) - OUT) / STAGE;
     static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
     static constexpr int TMEM_COLS = 2 * NT;
+    static constexpr int SUM_TOKENS = NT <= 16 ? 1 : 4;   // tokens a warp sums at a time
     static constexpr int SMEM = STAGES * STAGE + OUT + 1024;
 };
 
@@ -607,6 +641,7 @@ template <int NT>
 __global__ void __launch_bounds__(MoeDownCfg<NT>::THREADS, 1)
 moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const MoeParams p) {
     using C = MoeDownCfg<NT>;
+    constexpr int kSumTokens = C::SUM_TOKENS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
     float* out = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);   // [token][channel]
@@ -618,6 +653,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh, last_sh;
     __shared__ __align__(16) float col_s[4][NT];
+    __shared__ float sh_ring[4][kScaleRing][NT], sw_ring[4][kScaleRing];
     __shared__ ListSh list;
 
     const int warp = warp_index(), lane = threadIdx.x % 32;
@@ -752,6 +788,42 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const int q = warp & 3;
         const int ch = q * 32 + lane;
         float* cs = col_s[q];
+        // The step whose scales are asked for next.
+        int as = s_begin, akb = 0, ant = 0, aa = 0, abase = 0, acnt = 0;
+        const float* asw = nullptr;
+        if (s_begin < s_end) {
+            const int v0 = s_begin / p.kb2;
+            akb = s_begin - v0 * p.kb2;
+            ant = v0 / active;
+            aa = v0 - ant * active;
+        }
+        auto enter = [&] {                                  // its expert
+            abase = list.base[aa];
+            acnt = list.base[aa + 1] - abase;
+            asw = p.s2 + (static_cast<int64_t>(list.expert[aa]) * p.ht + ant) * p.kb2;
+        };
+        auto ask = [&] {
+            if (as < s_end) {
+                const int slot = (as - s_begin) % kScaleRing;
+#pragma unroll
+                for (int c = 0; c < NT; c += 32)
+                    if (c + lane < acnt)
+                        cp_async4(&sh_ring[q][slot][c + lane], p.hs + static_cast<int64_t>(akb) * p.rows_max + abase + c + lane);
+                if (lane == 0) cp_async4(&sw_ring[q][slot], asw + akb);
+                ++as;
+                if (++akb == p.kb2) {
+                    akb = 0;
+                    if (++aa == active) {
+                        aa = 0;
+                        ++ant;
+                    }
+                    if (as < s_end) enter();
+                }
+            }
+            cp_async_commit();
+        };
+        if (s_begin < s_end) enter();
+        for (int i = 0; i < kAhead; ++i) ask();
         float* oc = out + ch;
         if (active == 0) {                           // no token chose an expert: y is zero
             for (int nt = cta; nt < p.ht; nt += static_cast<int>(gridDim.x))
@@ -771,22 +843,11 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 const int v = s / p.kb2, k0 = s - v * p.kb2;
                 const int k1 = min(p.kb2, k0 + s1 - s);
                 const int a = v - nt * active;
-                const int e = list.expert[a], base = list.base[a];
-                const int cnt = list.base[a + 1] - base;
-                const float* sw = p.s2 + (static_cast<int64_t>(e) * p.ht + nt) * p.kb2;
+                const int base = list.base[a], cnt = list.base[a + 1] - base;
                 float2 acc[NT / 2];
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
                 constexpr int NS = (NT + 31) / 32;
-                float sh[NS], swk = __ldg(sw + k0);
-                auto fetch = [&](int kb) {
-#pragma unroll
-                    for (int c = 0; c < NS; ++c) {
-                        const int i = c * 32 + lane;
-                        sh[c] = i < cnt ? __ldcg(p.hs + static_cast<int64_t>(kb) * p.rows_max + base + i) : 0.f;
-                    }
-                };
-                fetch(k0);
                 int tk[NS];                      // the rows' tokens and weights, one row per lane
                 float wt[NS];
 #pragma unroll
@@ -796,14 +857,13 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     wt[c] = have ? __ldcg(p.row_weight + base + c * 32 + lane) : 0.f;
                 }
                 for (int kb = k0; kb < k1; ++kb) {
+                    ask();
+                    cp_async_wait<kAhead>();
                     __syncwarp();
+                    const int slot = (s + kb - k0 - s_begin) % kScaleRing;
 #pragma unroll
                     for (int c = 0; c < NS; ++c)
-                        if (c * 32 + lane < NT) cs[c * 32 + lane] = sh[c] * swk;
-                    if (kb + 1 < k1) {
-                        fetch(kb + 1);
-                        swk = __ldg(sw + kb + 1);
-                    }
+                        if (c * 32 + lane < NT) cs[c * 32 + lane] = sh_ring[q][slot][c * 32 + lane] * sw_ring[q][slot];
                     ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -843,20 +903,44 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 first = line.owner(tile0);
                 lastc = line.owner(tile1 - 1);
                 finish = arrive_last(&p.down_count[nt], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1, 128);
-                if (finish) {
-                    for (int t = 0; t < p.m; ++t) {
-                        float sum = 0.f;
-#pragma unroll 4
-                        for (int c = first; c <= lastc; ++c)
-                            sum += __ldcg(p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) +
-                                          t * kBM + ch);
-                        oc[t * kBM] = sum;
+            } else {
+                named_barrier(1, 128);               // every channel's sums are in shared memory
+            }
+            if (finish) {
+                // Four channels per lane, a token per warp: the sums over experts,
+                // or those of all contributors in the order of the CTAs.
+                const int n = nt * kBM + lane * 4;
+                for (int t = q; t < p.m; t += 4 * kSumTokens) {
+                    float4 v[kSumTokens];
+#pragma unroll
+                    for (int j = 0; j < kSumTokens; ++j) {
+                        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (first == lastc && t + 4 * j < p.m)
+                            v[j] = *reinterpret_cast<const float4*>(out + (t + 4 * j) * kBM + lane * 4);
                     }
+                    if (first != lastc) {
+#pragma unroll 4
+                        for (int c = first; c <= lastc; ++c) {
+                            const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) + lane * 4;
+#pragma unroll
+                            for (int j = 0; j < kSumTokens; ++j) {
+                                const int tj = min(t + 4 * j, p.m - 1);
+                                const float4 x = __ldcg(reinterpret_cast<const float4*>(src + tj * kBM));
+                                v[j].x += x.x;
+                                v[j].y += x.y;
+                                v[j].z += x.z;
+                                v[j].w += x.w;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < kSumTokens; ++j)
+                        if (t + 4 * j < p.m && n < p.hidden)
+                            *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t + 4 * j) * p.ldy + n) =
+                                make_uint2(pack_bf16(v[j].x, v[j].y), pack_bf16(v[j].z, v[j].w));
                 }
             }
-            if (finish && nt * kBM + ch < p.hidden)
-                for (int t = 0; t < p.m; ++t)
-                    p.y[t * p.ldy + nt * kBM + ch] = __float2bfloat16_rn(oc[t * kBM]);
+            named_barrier(1, 128);                   // before the sums of the next tile
         }
         __syncwarp();
     }
