@@ -154,41 +154,45 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restrict__ ids,
                    const float* __restrict__ weights, const MoeParams p) {
-    const int warp = warp_index(), lane = threadIdx.x % 32;
-    if (blockIdx.x + 1 < gridDim.x) {
-        // 256 columns (two groups) of every token; a warp takes a token at a time.
-        const int col = static_cast<int>(blockIdx.x) * 256 + lane * 8;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (blockIdx.x > 0) {
+        // 256 columns (two groups) of eight tokens, a warp each.
+        const int cols = (p.hidden + 255) / 256;
+        const int col = (static_cast<int>(blockIdx.x) - 1) % cols * 256 + lane * 8;
+        const int t = (static_cast<int>(blockIdx.x) - 1) / cols * 8 + warp;
         pdl_wait();
         pdl_launch_dependents();
-        for (int t = warp; t < p.m; t += 8) {
-            Eight<T> v;
-            if (col < p.hidden) v.load(X + static_cast<int64_t>(t) * ldx + col);
-            else v.zero();
-            float f[8];
-            v.values(f);
-            float a = absmax8(f);
+        if (t >= p.m) return;
+        Eight<T> v;
+        if (col < p.hidden) v.load(X + static_cast<int64_t>(t) * ldx + col);
+        else v.zero();
+        float f[8];
+        v.values(f);
+        float a = absmax8(f);
 #pragma unroll
-            for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            const BlockScale s = block_scale(a);
-            if (col < p.hidden) {
-                *reinterpret_cast<uint2*>(p.xq + static_cast<int64_t>(t) * p.hidden + col) =
-                    make_uint2(block_codes4(f[0], f[1], f[2], f[3], s), block_codes4(f[4], f[5], f[6], f[7], s));
-                if (lane % 16 == 0) p.xs[static_cast<int64_t>(col / kBlock) * p.m + t] = s.S;
-            }
+        for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const BlockScale s = block_scale(a);
+        if (col < p.hidden) {
+            *reinterpret_cast<uint2*>(p.xq + static_cast<int64_t>(t) * p.hidden + col) =
+                make_uint2(block_codes4(f[0], f[1], f[2], f[3], s), block_codes4(f[4], f[5], f[6], f[7], s));
+            if (lane % 16 == 0) p.xs[static_cast<int64_t>(col / kBlock) * p.m + t] = s.S;
         }
         return;
     }
-    // The last block: tokens of every expert as a bit mask (an expert that a
+    // The first block: tokens of every expert as a bit mask (an expert that a
     // token names twice has it once, with both weights), then the list.
     __shared__ unsigned long long mask_sh[kMaxExperts];
-    __shared__ int list_sh[kMaxExperts], base_sh[kMaxExperts];
-    __shared__ int active_sh, rows_sh;
+    __shared__ int base_sh[kMaxExperts];                 // by expert: its first row
+    __shared__ int ids_sh[kMaxTokens * kMoeMaxTopK];
+    __shared__ float weights_sh[kMaxTokens * kMoeMaxTopK];
     for (int e = threadIdx.x; e < p.experts; e += 256) mask_sh[e] = 0ull;
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     for (int i = threadIdx.x; i < p.rows_max; i += 256) {
         const int e = ids[i];
+        ids_sh[i] = e;
+        weights_sh[i] = weights[i];
         if (e >= 0 && e < p.experts) atomicOr(&mask_sh[e], 1ull << (i / p.top_k));
     }
     for (int i = threadIdx.x; i < min(p.experts, p.rows_max) * p.it; i += 256) p.up_count[i] = 0;
@@ -208,38 +212,33 @@ moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restri
             }
             if (c > 0) {
                 const int a = na + __popc(some & ((1u << lane) - 1u));
-                list_sh[a] = e;
-                base_sh[a] = nr + incl - c;
+                p.expert[a] = e;
+                p.base[a] = base_sh[e] = nr + incl - c;
             }
             na += __popc(some);
             nr += __shfl_sync(0xffffffffu, incl, 31);
         }
         if (lane == 0) {
-            active_sh = na;
-            rows_sh = nr;
+            p.head[0] = na;
+            p.base[na] = nr;
         }
     }
     __syncthreads();
-    const int na = active_sh;
-    if (threadIdx.x == 0) {
-        p.head[0] = na;
-        p.base[na] = rows_sh;
-    }
-    for (int a = threadIdx.x; a < na; a += 256) {
-        const int e = list_sh[a];
-        const unsigned long long mk = mask_sh[e];
-        p.expert[a] = e;
-        p.base[a] = base_sh[a];
-        int r = base_sh[a];
-        for (unsigned long long b = mk; b; b &= b - 1) {
-            const int t = __ffsll(static_cast<long long>(b)) - 1;
-            float w = 0.f;
-            for (int s = 0; s < p.top_k; ++s)
-                if (ids[t * p.top_k + s] == e) w += weights[t * p.top_k + s];
-            p.row_token[r] = t;
-            p.row_weight[r] = w;
-            ++r;
-        }
+    // A thread per choice: the first of a token's choices of an expert writes the row.
+    for (int i = threadIdx.x; i < p.rows_max; i += 256) {
+        const int e = ids_sh[i], t = i / p.top_k;
+        if (e < 0 || e >= p.experts) continue;
+        bool again = false;
+        float w = 0.f;
+        for (int s = t * p.top_k; s < (t + 1) * p.top_k; ++s)
+            if (ids_sh[s] == e) {
+                if (s < i) again = true;
+                w += weights_sh[s];
+            }
+        if (again) continue;
+        const int r = base_sh[e] + __popcll(mask_sh[e] & ((1ull << t) - 1ull));
+        p.row_token[r] = t;
+        p.row_weight[r] = w;
     }
 }
 
@@ -300,16 +299,17 @@ __device__ __forceinline__ bool arrive_last(int* counter, int parts, int* flag_s
 
 template <int NT>
 struct MoeUpCfg {
-    static constexpr int HALVES = NT >= 32 ? 2 : 1;
-    static constexpr int PROMO = 4 * HALVES;
-    static constexpr int THREADS = 32 * (2 + PROMO);
-    static constexpr int CW = NT / HALVES;            // token columns per promotion warp
+    // Two teams of four promotion warps take the tiles in turn: one finishes a
+    // tile (SwiGLU, scales and codes of h) while the other promotes the next.
+    // Each has two accumulators and barriers of its own: a barrier's parity
+    // only tells neighbouring phases apart.
+    static constexpr int THREADS = 32 * (2 + 8);
     static constexpr int B_BYTES = NT * kBKB;
     static constexpr int STAGE = 2 * kBM * kBKB + B_BYTES;
     // Up to 32 tokens two CTAs fit an SM, so that the down projection's can
     // take their place and ask for their weights while this kernel ends.
-    static constexpr int STAGES = NT <= 32 ? 3 : 5;
-    static constexpr int TMEM_COLS = 4 * NT;
+    static constexpr int STAGES = NT <= 32 ? 3 : 4;
+    static constexpr int TMEM_COLS = 8 * NT;
     static constexpr int SMEM = STAGES * STAGE + 1024;
 };
 
@@ -321,14 +321,14 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     uint8_t* smem = align1024(smem_raw);
     __shared__ __align__(8) uint64_t full_bar[C::STAGES];
     __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
-    __shared__ __align__(8) uint64_t tfull_bar[2];
-    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t tfull_bar[4];    // [team][accumulator]
+    __shared__ __align__(8) uint64_t tempty_bar[4];
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_sh, last_sh;
-    __shared__ __align__(16) float col_s[C::PROMO][2][C::CW];
-    __shared__ float amax_sh[C::HALVES][4][C::CW];
-    __shared__ float sx_ring[C::PROMO][kScaleRing][C::CW], sw_ring[C::PROMO][kScaleRing][2];
+    __shared__ int abort_sh, last_sh[2];
+    __shared__ __align__(16) float col_s[8][2][NT];
+    __shared__ float amax_sh[2][4][NT];
+    __shared__ float sx_ring[8][kScaleRing][NT], sw_ring[8][kScaleRing][2];
     __shared__ ListSh list;
     __shared__ uint8_t token_sh[kMaxTokens * kMoeMaxTopK];
 
@@ -338,9 +338,9 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 4; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], C::PROMO);
+            mbar_init(&tempty_bar[b], 4);
         }
         mbar_init(&drain_bar, 1);
         abort_sh = 0;
@@ -420,17 +420,21 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             // The whole warp runs the loop and one lane issues: descriptors then
             // stay in uniform registers.
             const bool leader = elect_one();
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            int n_even = 0, n_odd = 0;                     // steps of team 0 and of team 1
             bool ok = true;
+            const int u_first = s_begin / p.kb1;
             for (int s = s_begin; s < s_end && ok;) {
                 const int u = s / p.kb1, k0 = s - u * p.kb1;
                 const int k1 = min(p.kb1, k0 + s_end - s);
-                const int a = u / p.it;
+                const int a = u / p.it, team = (u - u_first) & 1;
                 const int cnt = list.base[a + 1] - list.base[a];
                 const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                int n = team ? n_odd : n_even;
+                for (int kb = k0; kb < k1; ++kb, ++n) {
+                    const int buf = team * 2 + (n & 1);
+                    if (!mbar_wait_short(&tempty_bar[buf], ((n >> 1) & 1) ^ 1, &abort_sh, p.status) ||
                         !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
                         ok = false;
                         break;
@@ -454,9 +458,9 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                         stage = 0;
                         phase ^= 1;
                     }
-                    buf ^= 1;
-                    if (buf == 0) bphase ^= 1;
                 }
+                if (team) n_odd = n;
+                else n_even = n;
                 s += k1 - k0;
             }
             if (!ok && leader) {
@@ -466,46 +470,48 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         }
         __syncwarp();
     } else {
-        const int q = warp & 3, half = (warp - 2) / 4;
+        const int q = warp & 3, team = (warp - 2) / 4;
         const int ch = q * 32 + lane;
-        const int c0 = half * C::CW;
+        const bool lead = (warp - 2) % 4 == 0 && lane == 0;
         float* cs = &col_s[warp - 2][0][0];
-        // The step whose scales are asked for next.
-        int as = s_begin, akb = 0, ait = 0, aa = -1, acn = 0, atok = 0;
+        constexpr int NS = (NT + 31) / 32;
+        // The team's step whose scales are asked for next.
+        const int u_first = s_begin / p.kb1;
+        int as = s_begin, akb = s_begin - u_first * p.kb1, au = u_first, acn = 0, asked = 0, used = 0;
+        int atok[NS];
         const float* asw = nullptr;
-        if (s_begin < s_end) {
-            const int u0 = s_begin / p.kb1;
-            akb = s_begin - u0 * p.kb1;
-            aa = u0 / p.it;
-            ait = u0 - aa * p.it;
+        if (team == 1) {
+            as = (u_first + 1) * p.kb1;
+            akb = 0;
+            ++au;
         }
         auto enter = [&] {                                  // its tile
-            const int row0 = list.base[aa] + c0;
-            acn = min(C::CW, list.base[aa + 1] - row0);
-            atok = lane < acn ? token_sh[row0 + lane] : 0;
-            asw = p.s13 + (static_cast<int64_t>(list.expert[aa]) * 2 * p.it + ait) * p.kb1;
+            const int a = au / p.it, base = list.base[a];
+            acn = list.base[a + 1] - base;
+#pragma unroll
+            for (int c = 0; c < NS; ++c) atok[c] = c * 32 + lane < acn ? token_sh[base + c * 32 + lane] : 0;
+            asw = p.s13 + (static_cast<int64_t>(list.expert[a]) * 2 * p.it + (au - a * p.it)) * p.kb1;
         };
         auto ask = [&] {
             if (as < s_end) {
-                const int slot = (as - s_begin) % kScaleRing;
-                if (lane < acn) cp_async4(&sx_ring[warp - 2][slot][lane], p.xs + static_cast<int64_t>(akb) * p.m + atok);
+                const int slot = asked++ % kScaleRing;
+#pragma unroll
+                for (int c = 0; c < NS; ++c)
+                    if (c * 32 + lane < acn)
+                        cp_async4(&sx_ring[warp - 2][slot][c * 32 + lane], p.xs + static_cast<int64_t>(akb) * p.m + atok[c]);
                 if (lane < 2) cp_async4(&sw_ring[warp - 2][slot][lane], asw + static_cast<int64_t>(lane) * p.it * p.kb1 + akb);
                 ++as;
-                if (++akb == p.kb1) {
+                if (++akb == p.kb1) {                       // the next tile is the other team's
                     akb = 0;
-                    if (++ait == p.it) {
-                        ait = 0;
-                        ++aa;
-                    }
+                    au += 2;
+                    as += p.kb1;
                     if (as < s_end) enter();
                 }
             }
             cp_async_commit();
         };
-        if (s_begin < s_end) enter();
+        if (as < s_end) enter();
         for (int i = 0; i < kAhead; ++i) ask();
-        int buf = 0;
-        uint32_t bphase = 0;
         // After a wait that ran out, the warps stop waiting and reading TMEM but
         // take the same barriers to the end (the status word tells the caller).
         bool ok = true;
@@ -513,74 +519,85 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             const int u = s / p.kb1, k0 = s - u * p.kb1;
             const int k1 = min(p.kb1, k0 + s_end - s);
             const int a = u / p.it, it = u - a * p.it;
-            const int row0 = list.base[a] + c0;             // this warp's columns are rows row0 ..
-            const int cn = min(C::CW, list.base[a + 1] - row0);   // and how many it has (may be none)
-            float2 g[C::CW / 2], w[C::CW / 2];
+            if (((u - u_first) & 1) != team) {
+                s += k1 - k0;
+                continue;
+            }
+            const int row0 = list.base[a], cn = list.base[a + 1] - row0;   // column i is row row0 + i
+            float2 g[NT / 2], w[NT / 2];
 #pragma unroll
-            for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < NT / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
             for (int kb = k0; kb < k1; ++kb) {
                 ask();
                 cp_async_wait<kAhead>();
                 __syncwarp();
-                const int slot = (s + kb - k0 - s_begin) % kScaleRing;
-                if (lane < C::CW) {
-                    const float sx = sx_ring[warp - 2][slot][lane];
-                    cs[lane] = sx * sw_ring[warp - 2][slot][0];
-                    cs[C::CW + lane] = sx * sw_ring[warp - 2][slot][1];
+                const int slot = used % kScaleRing;
+#pragma unroll
+                for (int c = 0; c < NS; ++c) {
+                    const int i = c * 32 + lane;
+                    if (i < NT) {
+                        const float sx = sx_ring[warp - 2][slot][i];
+                        cs[i] = sx * sw_ring[warp - 2][slot][0];
+                        cs[NT + i] = sx * sw_ring[warp - 2][slot][1];
+                    }
                 }
-                ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
+                const int buf = team * 2 + (used & 1);
+                ok = ok && mbar_wait_short(&tfull_bar[buf], (used >> 1) & 1, &abort_sh, p.status);
+                ++used;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 2 * NT + c0;
+                const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 2 * NT;
 #pragma unroll
-                for (int c = 0; c < C::CW / 16; ++c) {
+                for (int c = 0; c < NT / 16; ++c) {
                     if (c * 16 < cn) {
                         uint32_t rg[16], ru[16];
                         tmem_ld16(tb + c * 16, rg);
                         tmem_ld16(tb + NT + c * 16, ru);
                         tmem_ld_wait();
                         promote16(g + c * 8, rg, cs + c * 16);
-                        promote16(w + c * 8, ru, cs + C::CW + c * 16);
+                        promote16(w + c * 8, ru, cs + NT + c * 16);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tempty_bar[buf]);
-                buf ^= 1;
-                if (buf == 0) bphase ^= 1;
             }
             bool finish = true;
             if (k1 - k0 < p.kb1) {
                 // A piece of a tile: [cta][first or last tile][gate, up][column][channel].
                 float* mine = p.part + (static_cast<int64_t>(cta) * 2 + (k0 > 0 ? 0 : 1)) * (2 * NT * kBM) + ch;
 #pragma unroll
-                for (int i = 0; i < C::CW; ++i) {
+                for (int i = 0; i < NT; ++i) {
                     if (i < cn) {
-                        mine[(c0 + i) * kBM] = (i & 1) ? g[i / 2].y : g[i / 2].x;
-                        mine[(NT + c0 + i) * kBM] = (i & 1) ? w[i / 2].y : w[i / 2].x;
+                        mine[i * kBM] = (i & 1) ? g[i / 2].y : g[i / 2].x;
+                        mine[(NT + i) * kBM] = (i & 1) ? w[i / 2].y : w[i / 2].x;
                     }
                 }
                 const int first = line.owner(u * p.kb1), lastc = line.owner((u + 1) * p.kb1 - 1);
-                finish = arrive_last(&p.up_count[u], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1, 32 * C::PROMO);
+                finish = arrive_last(&p.up_count[u], lastc - first + 1, &last_sh[team], lead, 1 + team, 128);
                 if (finish) {
 #pragma unroll
-                    for (int i = 0; i < C::CW / 2; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
-                    for (int c = first; c <= lastc; ++c) {
-                        const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
-                        // All of a contributor's sums are asked for before any is added.
-                        float x[C::CW], v[C::CW];
+                    for (int c16 = 0; c16 < NT; c16 += 16) {
+                        if (c16 >= cn) break;
 #pragma unroll
-                        for (int i = 0; i < C::CW; ++i) {
-                            x[i] = i < cn ? __ldcg(src + (c0 + i) * kBM) : 0.f;
-                            v[i] = i < cn ? __ldcg(src + (NT + c0 + i) * kBM) : 0.f;
-                        }
+                        for (int i = c16 / 2; i < c16 / 2 + 8; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
+                        for (int c = first; c <= lastc; ++c) {
+                            const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
+                            // A contributor's sums are asked for together.
+                            float x[16], v[16];
 #pragma unroll
-                        for (int i = 0; i < C::CW / 2; ++i) {
-                            g[i].x += x[2 * i];
-                            g[i].y += x[2 * i + 1];
-                            w[i].x += v[2 * i];
-                            w[i].y += v[2 * i + 1];
+                            for (int i = 0; i < 16; ++i) {
+                                x[i] = c16 + i < cn ? __ldcg(src + (c16 + i) * kBM) : 0.f;
+                                v[i] = c16 + i < cn ? __ldcg(src + (NT + c16 + i) * kBM) : 0.f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                g[c16 / 2 + i].x += x[2 * i];
+                                g[c16 / 2 + i].y += x[2 * i + 1];
+                                w[c16 / 2 + i].x += v[2 * i];
+                                w[c16 / 2 + i].y += v[2 * i + 1];
+                            }
                         }
                     }
                 }
@@ -588,30 +605,38 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             if (finish) {
                 // h = silu(G) U of this tile: one scale group of h per token.
 #pragma unroll
-                for (int i = 0; i < C::CW; ++i) {
+                for (int i = 0; i < NT; ++i) {
                     if (i < cn) {
                         float& gi = (i & 1) ? g[i / 2].y : g[i / 2].x;
                         const float ui = (i & 1) ? w[i / 2].y : w[i / 2].x;
                         gi = gi / (1.0f + expf(-gi)) * ui;
                         const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(gi)));
-                        if (lane == 0) amax_sh[half][q][i] = __uint_as_float(am);
+                        if (lane == 0) amax_sh[team][q][i] = __uint_as_float(am);
                     }
                 }
-                named_barrier(2 + half, 128);
+                named_barrier(3 + team, 128);
+                // A lane computes a token's scale; the others take it from there.
+                BlockScale bs[NS];
 #pragma unroll
-                for (int i = 0; i < C::CW; ++i) {
+                for (int c = 0; c < NS; ++c) {
+                    const int i = c * 32 + lane < NT ? c * 32 + lane : 0;
+                    bs[c] = block_scale(fmaxf(fmaxf(amax_sh[team][0][i], amax_sh[team][1][i]),
+                                              fmaxf(amax_sh[team][2][i], amax_sh[team][3][i])));
+                    if (q == 0 && c * 32 + lane < cn) p.hs[static_cast<int64_t>(it) * p.rows_max + row0 + c * 32 + lane] = bs[c].S;
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
                     if (i < cn) {
-                        const int r = row0 + i;
-                        const float am = fmaxf(fmaxf(amax_sh[half][0][i], amax_sh[half][1][i]),
-                                               fmaxf(amax_sh[half][2][i], amax_sh[half][3][i]));
-                        const BlockScale bs = block_scale(am);
+                        BlockScale b;
+                        b.S = __shfl_sync(0xffffffffu, bs[i / 32].S, i % 32);
+                        b.R = __shfl_sync(0xffffffffu, bs[i / 32].R, i % 32);
+                        b.Rlo = __shfl_sync(0xffffffffu, bs[i / 32].Rlo, i % 32);
                         const float hi = (i & 1) ? g[i / 2].y : g[i / 2].x;
-                        p.hq[static_cast<int64_t>(r) * p.inter + it * kBM + ch] =
-                            static_cast<uint8_t>(block_codes4(hi, 0.f, 0.f, 0.f, bs) & 0xFFu);
-                        if (ch == 0) p.hs[static_cast<int64_t>(it) * p.rows_max + r] = bs.S;
+                        p.hq[static_cast<int64_t>(row0 + i) * p.inter + it * kBM + ch] =
+                            static_cast<uint8_t>(block_codes4(hi, 0.f, 0.f, 0.f, b) & 0xFFu);
                     }
                 }
-                named_barrier(2 + half, 128);   // amax_sh may be written again
+                named_barrier(3 + team, 128);   // amax_sh may be written again
             }
             s += k1 - k0;
         }
@@ -884,13 +909,23 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     buf ^= 1;
                     if (buf == 0) bphase ^= 1;
                 }
-                // The expert's weighted rows join the tile's sums (a thread owns its channel).
+                // The expert's weighted rows join the tile's sums (a thread owns its
+                // channel); its tokens differ, so 16 are loaded together.
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i < cnt) {
-                        const int t = __shfl_sync(0xffffffffu, tk[i / 32], i % 32);
-                        const float wi = __shfl_sync(0xffffffffu, wt[i / 32], i % 32);
-                        oc[t * kBM] = __fmaf_rn(wi, (i & 1) ? acc[i / 2].y : acc[i / 2].x, oc[t * kBM]);
+                for (int c16 = 0; c16 < NT; c16 += 16) {
+                    if (c16 < cnt) {
+                        int at[16];
+                        float wi[16], old[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            at[i] = __shfl_sync(0xffffffffu, tk[(c16 + i) / 32], (c16 + i) % 32) * kBM;
+                            wi[i] = __shfl_sync(0xffffffffu, wt[(c16 + i) / 32], (c16 + i) % 32);
+                            old[i] = oc[at[i]];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c16 + i < cnt)
+                                oc[at[i]] = __fmaf_rn(wi[i], (i & 1) ? acc[(c16 + i) / 2].y : acc[(c16 + i) / 2].x, old[i]);
                     }
                 }
                 s += k1 - k0;
@@ -1048,7 +1083,7 @@ q8_status launch(K kern, int blocks, int threads, int smem, cudaStream_t s, Args
 
 template <typename T>
 q8_status prepare(const MoeLayerArgs& a, const MoeParams& p, cudaStream_t s) {
-    return launch(moe_prepare_kernel<T>, static_cast<int>((a.hidden + 255) / 256) + 1, 256, 0, s,
+    return launch(moe_prepare_kernel<T>, static_cast<int>((a.hidden + 255) / 256 * ((a.m + 7) / 8)) + 1, 256, 0, s,
                   static_cast<const T*>(a.x), a.ldx, a.ids, a.weights, p);
 }
 
