@@ -263,17 +263,25 @@ struct Line {
     }
 };
 
-// The expert list in shared memory, copied by the whole block.
+// The expert list in shared memory, copied by the whole block in one round
+// trip: every entry there may be is read, what lies past the active ones is not
+// used.
 struct ListSh {
+    int active;
     int expert[kMaxExperts];
     int base[kMaxExperts + 1];
 };
 
-__device__ __forceinline__ void copy_list(ListSh& l, const MoeParams& p, int active) {
-    for (int a = threadIdx.x; a <= active; a += blockDim.x) {
-        if (a < active) l.expert[a] = __ldcg(p.expert + a);
-        l.base[a] = active > 0 ? __ldcg(p.base + a) : 0;
+__device__ __forceinline__ void copy_list(ListSh& l, uint8_t* token_sh, const MoeParams& p) {
+    const int most = min(p.experts, p.rows_max);
+    if (threadIdx.x == 0) l.active = __ldcg(p.head);
+    for (int a = threadIdx.x; a <= most; a += blockDim.x) {
+        if (a < most) l.expert[a] = __ldcg(p.expert + a);
+        l.base[a] = __ldcg(p.base + a);
     }
+    if (token_sh)
+        for (int r = threadIdx.x; r < p.rows_max; r += blockDim.x) token_sh[r] = static_cast<uint8_t>(__ldcg(p.row_token + r));
+    __syncthreads();
 }
 
 // The scales of a step are asked for kAhead steps before their use, across tile
@@ -283,17 +291,18 @@ constexpr int kAhead = 6, kScaleRing = 8;
 
 // Counts this CTA's arrival at a tile with `parts` contributors; true in the
 // one that arrives last, which then sees every contributor's sums.  Called by
-// the `threads` threads of the promotion warps, after each wrote its sums.
-__device__ __forceinline__ bool arrive_last(int* counter, int parts, int* flag_sh, bool leader, int barrier, int threads) {
-    __threadfence();
-    named_barrier(barrier, threads);
+// 128 threads after each wrote its sums; the leader's fences cover them all
+// (the barriers order the others' accesses before and after).
+__device__ __forceinline__ bool arrive_last(int* counter, int parts, int* flag_sh, bool leader, int barrier) {
+    named_barrier(barrier, 128);
     if (leader) {
+        __threadfence();
         *flag_sh = atomicAdd(counter, 1) == parts - 1;
         __threadfence();
     }
-    named_barrier(barrier, threads);
+    named_barrier(barrier, 128);
     const bool last = *flag_sh != 0;
-    named_barrier(barrier, threads);   // the flag may be written again
+    named_barrier(barrier, 128);   // the flag may be written again
     return last;
 }
 
@@ -359,12 +368,8 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     // complete here, before it waits for this kernel.
     pdl_launch_dependents();
 
-    const int active = __ldcg(p.head);
-    copy_list(list, p, active);
-    __syncthreads();
-    const int rows = list.base[active];
-    for (int r = threadIdx.x; r < rows; r += C::THREADS) token_sh[r] = static_cast<uint8_t>(__ldcg(p.row_token + r));
-    __syncthreads();
+    copy_list(list, token_sh, p);
+    const int active = list.active;
     const Line line(static_cast<long long>(active) * p.it * p.kb1);
     const int cta = static_cast<int>(blockIdx.x);
     const int s_begin = active > 0 && cta < line.ctas ? line.start(cta) : 0;
@@ -563,77 +568,96 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tempty_bar[buf]);
             }
+            // From here on the sums are in local memory, so that loops over the
+            // tokens need not be unrolled: unrolled, this part is tens of KB of
+            // code, and its instructions come from HBM while the weights stream
+            // through L2 (64 tokens: 36 us per tile against 2).
+            float tg[NT], tw[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                if (i < cn) {
+                    tg[i] = (i & 1) ? g[i / 2].y : g[i / 2].x;
+                    tw[i] = (i & 1) ? w[i / 2].y : w[i / 2].x;
+                }
             bool finish = true;
             if (k1 - k0 < p.kb1) {
                 // A piece of a tile: [cta][first or last tile][gate, up][column][channel].
                 float* mine = p.part + (static_cast<int64_t>(cta) * 2 + (k0 > 0 ? 0 : 1)) * (2 * NT * kBM) + ch;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i < cn) {
-                        mine[i * kBM] = (i & 1) ? g[i / 2].y : g[i / 2].x;
-                        mine[(NT + i) * kBM] = (i & 1) ? w[i / 2].y : w[i / 2].x;
-                    }
+#pragma unroll 1
+                for (int i = 0; i < cn; ++i) {
+                    mine[i * kBM] = tg[i];
+                    mine[(NT + i) * kBM] = tw[i];
                 }
                 const int first = line.owner(u * p.kb1), lastc = line.owner((u + 1) * p.kb1 - 1);
-                finish = arrive_last(&p.up_count[u], lastc - first + 1, &last_sh[team], lead, 1 + team, 128);
+                finish = arrive_last(&p.up_count[u], lastc - first + 1, &last_sh[team], lead, 1 + team);
                 if (finish) {
+                    // Four contributors' sums of two tokens are asked for together.
+                    auto part = [&](int c) {
+                        return p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
+                    };
+#pragma unroll 1
+                    for (int i = 0; i < cn; i += 2) {
+                        const int i1 = min(i + 1, cn - 1);
+                        float g0 = 0.f, g1 = 0.f, w0 = 0.f, w1 = 0.f;
+#pragma unroll 1
+                        for (int c = first; c <= lastc; c += 4) {
+                            float x[4][4];
 #pragma unroll
-                    for (int c16 = 0; c16 < NT; c16 += 16) {
-                        if (c16 >= cn) break;
-#pragma unroll
-                        for (int i = c16 / 2; i < c16 / 2 + 8; ++i) g[i] = w[i] = make_float2(0.f, 0.f);
-                        for (int c = first; c <= lastc; ++c) {
-                            const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
-                            // A contributor's sums are asked for together.
-                            float x[16], v[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                x[i] = c16 + i < cn ? __ldcg(src + (c16 + i) * kBM) : 0.f;
-                                v[i] = c16 + i < cn ? __ldcg(src + (NT + c16 + i) * kBM) : 0.f;
+                            for (int j = 0; j < 4; ++j) {
+                                const float* src = part(min(c + j, lastc));
+                                x[j][0] = __ldcg(src + i * kBM);
+                                x[j][1] = __ldcg(src + i1 * kBM);
+                                x[j][2] = __ldcg(src + (NT + i) * kBM);
+                                x[j][3] = __ldcg(src + (NT + i1) * kBM);
                             }
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                g[c16 / 2 + i].x += x[2 * i];
-                                g[c16 / 2 + i].y += x[2 * i + 1];
-                                w[c16 / 2 + i].x += v[2 * i];
-                                w[c16 / 2 + i].y += v[2 * i + 1];
-                            }
+                            for (int j = 0; j < 4; ++j)
+                                if (c + j <= lastc) {
+                                    g0 += x[j][0];
+                                    g1 += x[j][1];
+                                    w0 += x[j][2];
+                                    w1 += x[j][3];
+                                }
                         }
+                        tg[i1] = g1;
+                        tw[i1] = w1;
+                        tg[i] = i1 > i ? g0 : g1;
+                        tw[i] = i1 > i ? w0 : w1;
                     }
                 }
             }
             if (finish) {
                 // h = silu(G) U of this tile: one scale group of h per token.
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i < cn) {
-                        float& gi = (i & 1) ? g[i / 2].y : g[i / 2].x;
-                        const float ui = (i & 1) ? w[i / 2].y : w[i / 2].x;
-                        gi = gi / (1.0f + expf(-gi)) * ui;
-                        const uint32_t am = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(gi)));
-                        if (lane == 0) amax_sh[team][q][i] = __uint_as_float(am);
+#pragma unroll 1
+                for (int i = 0; i < cn; i += 2) {
+                    const int i1 = min(i + 1, cn - 1);
+                    const float g0 = tg[i], g1 = tg[i1];
+                    const float h0 = g0 / (1.0f + expf(-g0)) * tw[i], h1 = g1 / (1.0f + expf(-g1)) * tw[i1];
+                    const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h0)));
+                    const uint32_t m1 = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h1)));
+                    if (lane == 0) {
+                        amax_sh[team][q][i] = __uint_as_float(m0);
+                        amax_sh[team][q][i1] = __uint_as_float(m1);
                     }
+                    tg[i] = h0;
+                    if (i1 > i) tg[i1] = h1;
                 }
                 named_barrier(3 + team, 128);
                 // A lane computes a token's scale; the others take it from there.
-                BlockScale bs[NS];
-#pragma unroll
-                for (int c = 0; c < NS; ++c) {
-                    const int i = c * 32 + lane < NT ? c * 32 + lane : 0;
-                    bs[c] = block_scale(fmaxf(fmaxf(amax_sh[team][0][i], amax_sh[team][1][i]),
-                                              fmaxf(amax_sh[team][2][i], amax_sh[team][3][i])));
-                    if (q == 0 && c * 32 + lane < cn) p.hs[static_cast<int64_t>(it) * p.rows_max + row0 + c * 32 + lane] = bs[c].S;
-                }
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (i < cn) {
+#pragma unroll 1
+                for (int i0 = 0; i0 < cn; i0 += 32) {
+                    const int il = min(i0 + lane, NT - 1);
+                    const BlockScale bs = block_scale(fmaxf(fmaxf(amax_sh[team][0][il], amax_sh[team][1][il]),
+                                                            fmaxf(amax_sh[team][2][il], amax_sh[team][3][il])));
+                    if (q == 0 && i0 + lane < cn) p.hs[static_cast<int64_t>(it) * p.rows_max + row0 + i0 + lane] = bs.S;
+#pragma unroll 2
+                    for (int i = i0; i < min(cn, i0 + 32); ++i) {
                         BlockScale b;
-                        b.S = __shfl_sync(0xffffffffu, bs[i / 32].S, i % 32);
-                        b.R = __shfl_sync(0xffffffffu, bs[i / 32].R, i % 32);
-                        b.Rlo = __shfl_sync(0xffffffffu, bs[i / 32].Rlo, i % 32);
-                        const float hi = (i & 1) ? g[i / 2].y : g[i / 2].x;
+                        b.S = __shfl_sync(0xffffffffu, bs.S, i - i0);
+                        b.R = __shfl_sync(0xffffffffu, bs.R, i - i0);
+                        b.Rlo = __shfl_sync(0xffffffffu, bs.Rlo, i - i0);
                         p.hq[static_cast<int64_t>(row0 + i) * p.inter + it * kBM + ch] =
-                            static_cast<uint8_t>(block_codes4(hi, 0.f, 0.f, 0.f, b) & 0xFFu);
+                            static_cast<uint8_t>(block_codes4(tg[i], 0.f, 0.f, 0.f, b) & 0xFFu);
                     }
                 }
                 named_barrier(3 + team, 128);   // amax_sh may be written again
@@ -706,9 +730,8 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     pdl_launch_dependents();
 
     // The expert list was complete before the up projection let this kernel start.
-    const int active = __ldcg(p.head);
-    copy_list(list, p, active);
-    __syncthreads();
+    copy_list(list, nullptr, p);
+    const int active = list.active;
     const int tile_steps = active * p.kb2;           // of one output tile
     const Line line(static_cast<long long>(tile_steps) * p.ht);
     const int cta = static_cast<int>(blockIdx.x);
@@ -910,23 +933,27 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     if (buf == 0) bphase ^= 1;
                 }
                 // The expert's weighted rows join the tile's sums (a thread owns its
-                // channel); its tokens differ, so 16 are loaded together.
+                // channel); its tokens differ, so four are loaded together.  In
+                // local memory and rolled, as in the up projection.
+                float ta[NT];
 #pragma unroll
-                for (int c16 = 0; c16 < NT; c16 += 16) {
-                    if (c16 < cnt) {
-                        int at[16];
-                        float wi[16], old[16];
+                for (int i = 0; i < NT; ++i)
+                    if (i < cnt) ta[i] = (i & 1) ? acc[i / 2].y : acc[i / 2].x;
+#pragma unroll 1
+                for (int i0 = 0; i0 < cnt; i0 += 4) {
+                    int at[4];
+                    float v[4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            at[i] = __shfl_sync(0xffffffffu, tk[(c16 + i) / 32], (c16 + i) % 32) * kBM;
-                            wi[i] = __shfl_sync(0xffffffffu, wt[(c16 + i) / 32], (c16 + i) % 32);
-                            old[i] = oc[at[i]];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c16 + i < cnt)
-                                oc[at[i]] = __fmaf_rn(wi[i], (i & 1) ? acc[(c16 + i) / 2].y : acc[(c16 + i) / 2].x, old[i]);
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = min(i0 + e, cnt - 1);
+                        const bool high = NT > 32 && i >= 32;
+                        at[e] = __shfl_sync(0xffffffffu, high ? tk[NS - 1] : tk[0], i % 32) * kBM;
+                        const float wi = __shfl_sync(0xffffffffu, high ? wt[NS - 1] : wt[0], i % 32);
+                        v[e] = __fmaf_rn(wi, ta[i], oc[at[e]]);
                     }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i0 + e < cnt) oc[at[e]] = v[e];
                 }
                 s += k1 - k0;
             }
@@ -937,7 +964,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 for (int t = 0; t < p.m; ++t) mine[t * kBM] = oc[t * kBM];
                 first = line.owner(tile0);
                 lastc = line.owner(tile1 - 1);
-                finish = arrive_last(&p.down_count[nt], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1, 128);
+                finish = arrive_last(&p.down_count[nt], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1);
             } else {
                 named_barrier(1, 128);               // every channel's sums are in shared memory
             }
