@@ -263,6 +263,23 @@ struct Line {
     }
 };
 
+// The tiles of a CTA's steps [begin, end) in the order it takes them: the piece
+// of the tile that the next CTA goes on with first, then the piece of the tile
+// that an earlier CTA began, then the whole tiles, so that the wait for other
+// contributors' sums lies under the whole tiles' stream.
+struct Pieces {
+    int begin, end, steps, first, count;
+    bool tail;
+    __device__ __forceinline__ Pieces(int b, int e, int steps_per_tile) : begin(b), end(e), steps(steps_per_tile) {
+        first = b / steps_per_tile;
+        count = b < e ? (e - 1) / steps_per_tile - first + 1 : 0;
+        tail = e % steps_per_tile != 0;
+    }
+    __device__ __forceinline__ int tile(int i) const { return tail ? (i == 0 ? first + count - 1 : first + i - 1) : first + i; }
+    __device__ __forceinline__ int k0(int u) const { return max(begin - u * steps, 0); }
+    __device__ __forceinline__ int k1(int u) const { return min(end - u * steps, steps); }
+};
+
 // The expert list in shared memory, copied by the whole block in one round
 // trip: every entry there may be is read, what lies past the active ones is not
 // used.
@@ -374,6 +391,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
     const int cta = static_cast<int>(blockIdx.x);
     const int s_begin = active > 0 && cta < line.ctas ? line.start(cta) : 0;
     const int s_end = active > 0 && cta < line.ctas ? line.start(cta + 1) : 0;
+    const Pieces pieces(s_begin, s_end, p.kb1);
 
     if (warp == 0) {
         if (elect_one() && s_begin < s_end) {
@@ -383,9 +401,8 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int s = s_begin; s < s_end && ok;) {
-                const int u = s / p.kb1, k0 = s - u * p.kb1;
-                const int k1 = min(p.kb1, k0 + s_end - s);
+            for (int i = 0; i < pieces.count && ok; ++i) {
+                const int u = pieces.tile(i), k0 = pieces.k0(u), k1 = pieces.k1(u);
                 const int a = u / p.it;
                 const int row = list.expert[a] * 2 * p.inter + (u - a * p.it) * kBM;
                 const int base = list.base[a], cnt = list.base[a + 1] - base;
@@ -413,7 +430,6 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                         phase ^= 1;
                     }
                 }
-                s += k1 - k0;
             }
             if (!ok)   // the loads already issued land before the CTA leaves
                 for (int t = 0; t < C::STAGES; ++t)
@@ -429,11 +445,9 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
             uint32_t phase = 0;
             int n_even = 0, n_odd = 0;                     // steps of team 0 and of team 1
             bool ok = true;
-            const int u_first = s_begin / p.kb1;
-            for (int s = s_begin; s < s_end && ok;) {
-                const int u = s / p.kb1, k0 = s - u * p.kb1;
-                const int k1 = min(p.kb1, k0 + s_end - s);
-                const int a = u / p.it, team = (u - u_first) & 1;
+            for (int i = 0; i < pieces.count && ok; ++i) {
+                const int u = pieces.tile(i), k0 = pieces.k0(u), k1 = pieces.k1(u);
+                const int a = u / p.it, team = i & 1;
                 const int cnt = list.base[a + 1] - list.base[a];
                 const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
                 int n = team ? n_odd : n_even;
@@ -466,7 +480,6 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 }
                 if (team) n_odd = n;
                 else n_even = n;
-                s += k1 - k0;
             }
             if (!ok && leader) {
                 tc_commit(&drain_bar);
@@ -481,53 +494,41 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
         float* cs = &col_s[warp - 2][0][0];
         constexpr int NS = (NT + 31) / 32;
         // The team's step whose scales are asked for next.
-        const int u_first = s_begin / p.kb1;
-        int as = s_begin, akb = s_begin - u_first * p.kb1, au = u_first, acn = 0, asked = 0, used = 0;
+        int ai = team, akb = 0, aend = 0, acn = 0, asked = 0, used = 0;
         int atok[NS];
         const float* asw = nullptr;
-        if (team == 1) {
-            as = (u_first + 1) * p.kb1;
-            akb = 0;
-            ++au;
-        }
         auto enter = [&] {                                  // its tile
-            const int a = au / p.it, base = list.base[a];
+            const int au = pieces.tile(ai), a = au / p.it, base = list.base[a];
             acn = list.base[a + 1] - base;
 #pragma unroll
             for (int c = 0; c < NS; ++c) atok[c] = c * 32 + lane < acn ? token_sh[base + c * 32 + lane] : 0;
+            akb = pieces.k0(au);
+            aend = pieces.k1(au);
             asw = p.s13 + (static_cast<int64_t>(list.expert[a]) * 2 * p.it + (au - a * p.it)) * p.kb1;
         };
         auto ask = [&] {
-            if (as < s_end) {
+            if (ai < pieces.count) {
                 const int slot = asked++ % kScaleRing;
 #pragma unroll
                 for (int c = 0; c < NS; ++c)
                     if (c * 32 + lane < acn)
                         cp_async4(&sx_ring[warp - 2][slot][c * 32 + lane], p.xs + static_cast<int64_t>(akb) * p.m + atok[c]);
                 if (lane < 2) cp_async4(&sw_ring[warp - 2][slot][lane], asw + static_cast<int64_t>(lane) * p.it * p.kb1 + akb);
-                ++as;
-                if (++akb == p.kb1) {                       // the next tile is the other team's
-                    akb = 0;
-                    au += 2;
-                    as += p.kb1;
-                    if (as < s_end) enter();
+                if (++akb == aend) {                        // the next tile is the other team's
+                    ai += 2;
+                    if (ai < pieces.count) enter();
                 }
             }
             cp_async_commit();
         };
-        if (as < s_end) enter();
+        if (ai < pieces.count) enter();
         for (int i = 0; i < kAhead; ++i) ask();
         // After a wait that ran out, the warps stop waiting and reading TMEM but
         // take the same barriers to the end (the status word tells the caller).
         bool ok = true;
-        for (int s = s_begin; s < s_end;) {
-            const int u = s / p.kb1, k0 = s - u * p.kb1;
-            const int k1 = min(p.kb1, k0 + s_end - s);
+        for (int i = team; i < pieces.count; i += 2) {
+            const int u = pieces.tile(i), k0 = pieces.k0(u), k1 = pieces.k1(u);
             const int a = u / p.it, it = u - a * p.it;
-            if (((u - u_first) & 1) != team) {
-                s += k1 - k0;
-                continue;
-            }
             const int row0 = list.base[a], cn = list.base[a + 1] - row0;   // column i is row row0 + i
             float2 g[NT / 2], w[NT / 2];
 #pragma unroll
@@ -662,7 +663,6 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 }
                 named_barrier(3 + team, 128);   // amax_sh may be written again
             }
-            s += k1 - k0;
         }
         __syncwarp();
     }
@@ -675,39 +675,41 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
 
 template <int NT>
 struct MoeDownCfg {
-    static constexpr int THREADS = 192;
+    static constexpr int THREADS = 32 * (2 + 8);      // four promotion warps, four that only help to sum
     static constexpr int B_BYTES = NT * kBKB;
     static constexpr int STAGE = kBM * kBKB + B_BYTES;
     static constexpr int OUT = NT * kBM * 4;          // the tile's sums over experts
-    static constexpr int STAGES_RAW = ((NT <= 32 ? 103 * 1024 : 200 * 1024) - OUT) / STAGE;
-    static constexpr int STAGES = STAGES_RAW > 10 ? 10 : STAGES_RAW;
+    static constexpr int MAX_STAGES = NT <= 32 ? 9 : 7;
+    // Few steps: a ring that fits an SM beside a CTA of the up projection, so
+    // that the first weights are on their way while that one ends.
+    static constexpr int FEW_STAGES = NT <= 16 ? 5 : NT <= 32 ? 4 : 7;
     static constexpr int TMEM_COLS = 2 * NT;
-    static constexpr int SUM_TOKENS = NT <= 16 ? 1 : 4;   // tokens a warp sums at a time
-    static constexpr int SMEM = STAGES * STAGE + OUT + 1024;
+    static constexpr int SUM_TOKENS = 4;              // tokens a warp sums at a time
+    static constexpr int smem(int stages) { return stages * STAGE + OUT + 1024; }
 };
 
 template <int NT>
 __global__ void __launch_bounds__(MoeDownCfg<NT>::THREADS, 1)
-moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const MoeParams p) {
+moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const MoeParams p,
+                int nstages) {
     using C = MoeDownCfg<NT>;
-    constexpr int kSumTokens = C::SUM_TOKENS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    float* out = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);   // [token][channel]
-    __shared__ __align__(8) uint64_t full_bar[C::STAGES];
-    __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
+    float* out = reinterpret_cast<float*>(smem + nstages * C::STAGE);   // [token][channel]
+    __shared__ __align__(8) uint64_t full_bar[C::MAX_STAGES];
+    __shared__ __align__(8) uint64_t empty_bar[C::MAX_STAGES];
     __shared__ __align__(8) uint64_t tfull_bar[2];
     __shared__ __align__(8) uint64_t tempty_bar[2];
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_sh, last_sh;
+    __shared__ int abort_sh, last_sh, sum_sh[3];   // sum_sh: whether to sum, over which CTAs
     __shared__ __align__(16) float col_s[4][NT];
     __shared__ float sh_ring[4][kScaleRing][NT], sw_ring[4][kScaleRing];
     __shared__ ListSh list;
 
     const int warp = warp_index(), lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < nstages; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], 1);
         }
@@ -738,6 +740,42 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int s_begin = active > 0 && cta < line.ctas ? line.start(cta) : 0;
     const int s_end = active > 0 && cta < line.ctas ? line.start(cta + 1) : 0;
 
+    // The finished rows of an output tile, four channels per lane and a token
+    // per warp: the sums over experts, or those of all contributors in the order
+    // of the CTAs.
+    auto sum_tile = [&](int nt, int first, int lastc) {
+        const int n = nt * kBM + lane * 4, tile0 = nt * tile_steps;
+#pragma unroll 1
+        for (int t = warp - 2; t < p.m; t += 8 * C::SUM_TOKENS) {
+            float4 v[C::SUM_TOKENS];
+#pragma unroll
+            for (int j = 0; j < C::SUM_TOKENS; ++j) {
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (first == lastc && t + 8 * j < p.m)
+                    v[j] = *reinterpret_cast<const float4*>(out + (t + 8 * j) * kBM + lane * 4);
+            }
+            if (first != lastc) {
+#pragma unroll 4
+                for (int c = first; c <= lastc; ++c) {
+                    const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) + lane * 4;
+#pragma unroll
+                    for (int j = 0; j < C::SUM_TOKENS; ++j) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + min(t + 8 * j, p.m - 1) * kBM));
+                        v[j].x += x.x;
+                        v[j].y += x.y;
+                        v[j].z += x.z;
+                        v[j].w += x.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < C::SUM_TOKENS; ++j)
+                if (t + 8 * j < p.m && n < p.hidden)
+                    *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t + 8 * j) * p.ldy + n) =
+                        make_uint2(pack_bf16(v[j].x, v[j].y), pack_bf16(v[j].z, v[j].w));
+        }
+    };
+
     if (warp == 0) {
         if (elect_one() && s_begin < s_end) {
             tma_prefetch_desc(&tmW);
@@ -746,7 +784,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             bool ok = true;
             // Pass 0 asks for the first ring's weights, before the up
             // projection is done; pass 1 for everything else.
-            const int first = min(s_end - s_begin, C::STAGES);
+            const int first = min(s_end - s_begin, nstages);
             for (int pass = 0; pass < 2 && ok; ++pass) {
                 if (pass == 1) pdl_wait();
                 int stage = 0;
@@ -775,7 +813,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                         if (pass == 1)
                             for (int b = 0; b < boxes; ++b)
                                 tma_load_2d(sa + kBM * kBKB + b * 16 * kBKB, &tmH, &full_bar[stage], kb * kBKB, base + b * 16);
-                        if (++stage == C::STAGES) {
+                        if (++stage == nstages) {
                             stage = 0;
                             phase ^= 1;
                         }
@@ -783,7 +821,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 }
             }
             if (!ok)
-                for (int t = 0; t < C::STAGES; ++t)
+                for (int t = 0; t < nstages; ++t)
                     if (issued & (1u << t)) mbar_wait(&full_bar[t], (last_par >> t) & 1, nullptr, nullptr);
         }
         __syncwarp();
@@ -816,7 +854,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                         tc_commit(&empty_bar[stage]);
                     }
                     __syncwarp();
-                    if (++stage == C::STAGES) {
+                    if (++stage == nstages) {
                         stage = 0;
                         phase ^= 1;
                     }
@@ -831,6 +869,16 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             }
         }
         __syncwarp();
+    } else if (warp >= 6) {
+        // The helpers of the sums over contributors.
+        pdl_wait();
+        for (int s = s_begin; s < s_end;) {
+            const int nt = s / tile_steps;
+            named_barrier(2, 256);
+            if (sum_sh[0]) sum_tile(nt, sum_sh[1], sum_sh[2]);
+            named_barrier(2, 256);
+            s = min((nt + 1) * tile_steps, s_end);
+        }
     } else {
         pdl_wait();
         const int q = warp & 3;
@@ -965,44 +1013,15 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 first = line.owner(tile0);
                 lastc = line.owner(tile1 - 1);
                 finish = arrive_last(&p.down_count[nt], lastc - first + 1, &last_sh, warp == 2 && lane == 0, 1);
-            } else {
-                named_barrier(1, 128);               // every channel's sums are in shared memory
             }
-            if (finish) {
-                // Four channels per lane, a token per warp: the sums over experts,
-                // or those of all contributors in the order of the CTAs.
-                const int n = nt * kBM + lane * 4;
-                for (int t = q; t < p.m; t += 4 * kSumTokens) {
-                    float4 v[kSumTokens];
-#pragma unroll
-                    for (int j = 0; j < kSumTokens; ++j) {
-                        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (first == lastc && t + 4 * j < p.m)
-                            v[j] = *reinterpret_cast<const float4*>(out + (t + 4 * j) * kBM + lane * 4);
-                    }
-                    if (first != lastc) {
-#pragma unroll 4
-                        for (int c = first; c <= lastc; ++c) {
-                            const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) + lane * 4;
-#pragma unroll
-                            for (int j = 0; j < kSumTokens; ++j) {
-                                const int tj = min(t + 4 * j, p.m - 1);
-                                const float4 x = __ldcg(reinterpret_cast<const float4*>(src + tj * kBM));
-                                v[j].x += x.x;
-                                v[j].y += x.y;
-                                v[j].z += x.z;
-                                v[j].w += x.w;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < kSumTokens; ++j)
-                        if (t + 4 * j < p.m && n < p.hidden)
-                            *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t + 4 * j) * p.ldy + n) =
-                                make_uint2(pack_bf16(v[j].x, v[j].y), pack_bf16(v[j].z, v[j].w));
-                }
+            if (warp == 2 && lane == 0) {
+                sum_sh[0] = finish;
+                sum_sh[1] = first;
+                sum_sh[2] = lastc;
             }
-            named_barrier(1, 128);                   // before the sums of the next tile
+            named_barrier(2, 256);                   // every channel's sums are in shared memory
+            if (finish) sum_tile(nt, first, lastc);
+            named_barrier(2, 256);                   // before the sums of the next tile
         }
         __syncwarp();
     }
@@ -1125,7 +1144,12 @@ q8_status products(const MoeLayerArgs& a, const MoeParams& p, cudaStream_t s) {
     const int ctas = sm_count() < kMoeMaxCtas ? sm_count() : static_cast<int>(kMoeMaxCtas);
     const q8_status st = launch(moe_up_kernel<NT>, ctas, MoeUpCfg<NT>::THREADS, MoeUpCfg<NT>::SMEM, s, tW13, tX, p);
     if (st != Q8_OK) return st;
-    return launch(moe_down_kernel<NT>, ctas, MoeDownCfg<NT>::THREADS, MoeDownCfg<NT>::SMEM, s, tW2, tH, p);
+    // Enough steps for a long ring to pay (the active experts are not known
+    // here: as many as there are choices, at most all).
+    using D = MoeDownCfg<NT>;
+    const int64_t steps = static_cast<int64_t>(p.rows_max < p.experts ? p.rows_max : p.experts) * p.ht * p.kb2 / ctas;
+    const int stages = steps > 32 ? D::MAX_STAGES : D::FEW_STAGES;
+    return launch(moe_down_kernel<NT>, ctas, D::THREADS, D::smem(stages), s, tW2, tH, p, stages);
 }
 
 }  // namespace
