@@ -469,20 +469,26 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
 // 128 output channels and up to NT tokens per cluster; the CTAs of a cluster
 // share the K groups and push their fp32 sums, four tokens of a channel at a
 // time, to the rank that finishes those tokens, which adds them in rank order.
-// One warp runs these few-token phases at an instruction every nine cycles or
-// so, so from 32 tokens on two sets of four warps take half the columns each.
+// A promotion is a chain of about 1000 cycles (barrier, scales, TMEM load,
+// sums), longer than an SM's share of the weight stream takes per group.  With
+// 32 or 64 tokens two teams of four warps therefore take the groups in turn, each
+// with two accumulators and sums of its own (48x14336x4096: 21.3 -> 17.5 us);
+// with 128, whose sums would not fit twice, two sets of warps take half the
+// columns each; with 16 one team will do, and leaves room for two CTAs per SM.
 // With QX the activation arrives unquantized and eight more warps quantize it
 // on its way into the stages (the codes are those of the activation
 // quantizer): a warp takes four tokens of one K group, and the groups go
-// round the warps, since one such piece is a chain of about 1000 cycles.
-//   warp 0 TMA, warp 1 MMA, then 4 or 8 promotion warps, then the quantizing ones.
+// round the warps, since one such piece is a chain of about 1000 cycles too.
+//   warp 0 TMA, warp 1 MMA, then the promotion warps, then the quantizing ones.
 
 constexpr int kQxWarps = 8;
 
 template <int NT, bool QX>
 struct BlockDecodeCfg {
-    static constexpr int HALVES = NT >= 32 ? 2 : 1;
-    static constexpr int PROMO = 4 * HALVES;
+    static constexpr int TEAMS = NT == 32 || NT == 64 ? 2 : 1;
+    static constexpr int HALVES = NT == 128 ? 2 : 1;
+    static constexpr int SETS = TEAMS * HALVES;  // sets of four promotion warps
+    static constexpr int PROMO = 4 * SETS;
     static constexpr int THREADS = 32 * (2 + PROMO + (QX ? kQxWarps : 0));
     static constexpr int CW = NT / HALVES;       // columns per promotion warp
     static constexpr int QUADS = NT / 4;
@@ -491,9 +497,9 @@ struct BlockDecodeCfg {
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int MAX_STAGES = NT <= 64 ? 8 : 5;
     // Scales of groups quantized on the way: a stage is refilled when its MMA
-    // is done, with the promotion at most two groups behind the MMA.
-    static constexpr int SX_RING = MAX_STAGES + 2;
-    static constexpr int TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+    // is done, with the promotion at most four groups behind the MMA.
+    static constexpr int SX_RING = MAX_STAGES + 4;
+    static constexpr int TMEM_COLS = 2 * TEAMS * NT;   // at least the 32 an allocation takes
     static_assert(!QX || NT == 16, "the quantizing warps cover 16 tokens");
 };
 
@@ -505,11 +511,11 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     using C = BlockDecodeCfg<NT, QX>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    float4* red = reinterpret_cast<float4*>(smem + nstages * C::STAGE);   // [rank][quads owned][128 channels]
+    float4* red = reinterpret_cast<float4*>(smem + nstages * C::STAGE);   // [rank][team][quads owned][128 channels]
     __shared__ __align__(8) uint64_t full_bar[C::MAX_STAGES];
     __shared__ __align__(8) uint64_t empty_bar[C::MAX_STAGES];
-    __shared__ __align__(8) uint64_t tfull_bar[2];
-    __shared__ __align__(8) uint64_t tempty_bar[2];
+    __shared__ __align__(8) uint64_t tfull_bar[2 * C::TEAMS];    // [team][accumulator]
+    __shared__ __align__(8) uint64_t tempty_bar[2 * C::TEAMS];
     __shared__ __align__(8) uint64_t drain_bar;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
@@ -534,9 +540,9 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             mbar_init(&full_bar[s], QX ? 1 + quads : 1);   // TMA (and the quantized quads)
             mbar_init(&empty_bar[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 2 * C::TEAMS; ++b) {
             mbar_init(&tfull_bar[b], 1);
-            mbar_init(&tempty_bar[b], C::PROMO);
+            mbar_init(&tempty_bar[b], C::PROMO / C::TEAMS);
         }
         if constexpr (QX)
             for (int s = 0; s < C::SX_RING; ++s) mbar_init(&sx_bar[s], quads);
@@ -600,11 +606,12 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         {
             const bool leader = elect_one();   // one lane issues, as in the pair kernel
             const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((mt + 15) / 16 * 16));
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
+            int stage = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int i = 0; i < my_kb; ++i) {
-                if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
+                const int n = i / C::TEAMS, buf = i % C::TEAMS * 2 + (n & 1);
+                if (!mbar_wait_short(&tempty_bar[buf], ((n >> 1) & 1) ^ 1, &abort_sh, p.status) ||
                     !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
                     ok = false;
                     break;
@@ -625,8 +632,6 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                     stage = 0;
                     phase ^= 1;
                 }
-                buf ^= 1;
-                if (buf == 0) bphase ^= 1;
             }
             if (!ok && leader) {
                 tc_commit(&drain_bar);
@@ -635,32 +640,31 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         }
         __syncwarp();
     } else if (warp < 2 + C::PROMO) {
-        const int q = warp & 3, half = (warp - 2) / 4;
+        const int q = warp & 3, set = (warp - 2) / 4;
+        const int team = C::TEAMS == 2 ? set : 0;
         const int ch = q * 32 + lane;
-        const int c0 = half * C::CW;                    // this warp's first token column
+        const int c0 = C::HALVES == 2 ? set * C::CW : 0; // this warp's first token column
         const int cn = min(C::CW, mt - c0);             // and how many it has (may be none)
-        const float* sw = p.sw + static_cast<int64_t>(tn) * num_kb;
+        const float* sw = p.sw + static_cast<int64_t>(tn) * num_kb + kb0;
         float* cs = col_s[warp - 2];
         float2 acc[C::CW / 2];
 #pragma unroll
         for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
         constexpr int NS = (C::CW + 31) / 32;           // column scales per lane
-        float sxv[NS], swk = my_kb > 0 ? __ldg(sw + kb0) : 0.f;
-        auto fetch_sx = [&](int kb) {
+        float sxv[NS], swk = team < my_kb ? __ldg(sw + team) : 0.f;
+        auto fetch_sx = [&](int i) {
 #pragma unroll
             for (int c = 0; c < NS; ++c) {
                 const int t = c * 32 + lane;
-                sxv[c] = t < cn ? __ldg(p.sx + static_cast<int64_t>(kb) * p.m + t0 + c0 + t) : 0.f;
+                sxv[c] = t < cn ? __ldg(p.sx + static_cast<int64_t>(kb0 + i) * p.m + t0 + c0 + t) : 0.f;
             }
         };
         if constexpr (!QX) {
             pdl_wait();
-            if (my_kb > 0) fetch_sx(kb0);
+            if (team < my_kb) fetch_sx(team);
         }
-        int buf = 0;
-        uint32_t bphase = 0;
-        for (int i = 0; i < my_kb; ++i) {
-            const int kb = kb0 + i;
+        for (int i = team; i < my_kb; i += C::TEAMS) {
+            const int n = i / C::TEAMS, buf = team * 2 + (n & 1);
             if constexpr (QX) {
                 if (!mbar_wait_short(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
                 if (lane < C::CW) cs[lane] = lane < cn ? sx_ring[i % C::SX_RING][lane] * swk : 0.f;
@@ -670,30 +674,29 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                     const int t = c * 32 + lane;
                     if (t < C::CW) cs[t] = sxv[c] * swk;
                 }
-                if (i + 1 < my_kb) fetch_sx(kb + 1);
+                if (i + C::TEAMS < my_kb) fetch_sx(i + C::TEAMS);
             }
-            if (i + 1 < my_kb) swk = __ldg(sw + kb + 1);
-            if (!mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
+            if (i + C::TEAMS < my_kb) swk = __ldg(sw + i + C::TEAMS);
+            if (!mbar_wait_short(&tfull_bar[buf], (n >> 1) & 1, &abort_sh, p.status)) break;
             __syncwarp();
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + c0;
+            constexpr int LW = C::CW >= 32 ? 32 : 16;   // columns per TMEM load
 #pragma unroll
-            for (int c = 0; c < C::CW / 16; ++c) {
-                if (c * 16 < cn) {
-                    uint32_t r[16];
-                    tmem_ld16(tb + c * 16, r);
+            for (int c = 0; c < C::CW / LW; ++c) {
+                if (c * LW < cn) {
+                    uint32_t r[LW];
+                    tmem_ld(tb + c * LW, r);
                     tmem_ld_wait();
-                    promote16(acc + c * 8, r, cs + c * 16);
+                    promote(acc + c * (LW / 2), r, cs + c * LW);
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty_bar[buf]);
-            buf ^= 1;
-            if (buf == 0) bphase ^= 1;
         }
-        // Quad g of the tile goes to rank g % splits, slot [rank][g / splits][channel].
-        const uint32_t dst = smem_addr(red) + (rank * qpo * kBM + ch) * 16u;
+        // Quad g of the tile goes to rank g % splits, slot [rank][team][g / splits][channel].
+        const uint32_t dst = smem_addr(red) + ((rank * C::TEAMS + team) * qpo * kBM + ch) * 16u;
         uint32_t owner = static_cast<uint32_t>(c0 / 4 % splits), off = static_cast<uint32_t>(c0 / 4 / splits) * (kBM * 16u);
 #pragma unroll
         for (int g = 0; g < C::CW / 4; ++g) {
@@ -752,14 +755,14 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     cluster_sync();
 
     if (warp >= 2 && warp < 2 + C::PROMO) {
-        const int ch = (warp & 3) * 32 + lane, half = (warp - 2) / 4;
+        const int ch = (warp & 3) * 32 + lane, set = (warp - 2) / 4;
         const int n = tn * kBM + ch;
         if constexpr (QX) pdl_wait();   // Y may still be read by the previous kernel
         if (n < p.n && !abort_sh) {
             const float bias = p.bias ? p.bias[n] : 0.f;
-            for (int sl = half, g = static_cast<int>(rank) + half * splits; g < quads; sl += C::HALVES, g += C::HALVES * splits) {
+            for (int sl = set, g = static_cast<int>(rank) + set * splits; g < quads; sl += C::SETS, g += C::SETS * splits) {
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int r = 0; r < splits; ++r) {
+                for (int r = 0; r < splits * C::TEAMS; ++r) {
                     const float4 v = red[(r * qpo + sl) * kBM + ch];
                     s.x = __fadd_rn(s.x, v.x);
                     s.y = __fadd_rn(s.y, v.y);
@@ -880,7 +883,7 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
     const int per = (num_kb + want - 1) / want;
     const int splits = (num_kb + per - 1) / per;
     const int quads = ((a.m < NT ? static_cast<int>(a.m) : NT) + 3) / 4;
-    const int red = splits * ((quads + splits - 1) / splits) * kBM * 16;
+    const int red = splits * C::TEAMS * ((quads + splits - 1) / splits) * kBM * 16;
     const int budget = (tiles_n * tiles_t * splits > sm_count() ? 113 : 220) * 1024 - 4 * 1024 - red;
     int nstages = budget / C::STAGE;
     if (nstages > C::MAX_STAGES) nstages = C::MAX_STAGES;
@@ -911,14 +914,16 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
 }
 
 // Tile width: the persistent grid's makespan, waves x (BN + a tile's fixed cost
-// of about 64 columns' worth), the wider tile on ties.
+// of about 64 columns' worth), the narrower tile on ties (16 experts x 2048 x
+// 4096, 4096 tokens: 65 us with 128 columns, 74 with 256; 1024x4096x4096: 26.6
+// and 18.9, 2048x14336x4096: 150 and 142).
 bool wide_tiles(int64_t row_tiles, int64_t n) {
     const int64_t sms = sm_count();
     auto cost = [&](int64_t bn) {
         const int64_t tiles = row_tiles * ((n + bn - 1) / bn);
         return ((tiles + sms - 1) / sms) * (bn + 64);
     };
-    return cost(256) <= cost(128);
+    return cost(256) < cost(128);
 }
 
 }  // namespace
@@ -933,7 +938,10 @@ cudaError_t launch_block_quant(const BlockQuantArgs& a, bool weight, cudaStream_
 
 q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     if (a.offsets) {
-        const int64_t rows = (a.m + kBM - 1) / kBM + a.experts / 2;
+        // Row tiles, estimated: half a partial tile per expert on top of the
+        // full ones, and one for every expert where they average fewer rows.
+        const int64_t full = (a.m + kBM - 1) / kBM, some = a.experts < a.m ? a.experts : a.m;
+        const int64_t rows = full + a.experts / 2 > some ? full + a.experts / 2 : some;
         return wide_tiles(rows, a.n) ? run_block_tile<256, true>(a, s) : run_block_tile<128, true>(a, s);
     }
     if (a.x) {   // quantized on the way

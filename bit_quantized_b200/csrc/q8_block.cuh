@@ -130,10 +130,14 @@ __device__ __forceinline__ void promote(float2* acc, const uint32_t (&r)[32], fl
             : "r"(r[2 * i]), "r"(r[2 * i + 1]), "l"(s2));
 }
 
-// The same for 16 columns with a scale per column, from 16-byte-aligned shared memory.
-__device__ __forceinline__ void promote16(float2* acc, const uint32_t (&r)[16], const float* s) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+
+// The same for N columns with a scale per column, from 16-byte-aligned shared memory.
+template <int N>
+__device__ __forceinline__ void promote(float2* acc, const uint32_t (&r)[N], const float* s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 4; ++i) {
         const float4 v = *reinterpret_cast<const float4*>(s + 4 * i);
         acc[2 * i] = __ffma2_rn(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])),
                                 make_float2(v.x, v.y), acc[2 * i]);

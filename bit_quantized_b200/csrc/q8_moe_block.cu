@@ -561,8 +561,8 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                         tmem_ld16(tb + c * 16, rg);
                         tmem_ld16(tb + NT + c * 16, ru);
                         tmem_ld_wait();
-                        promote16(g + c * 8, rg, cs + c * 16);
-                        promote16(w + c * 8, ru, cs + NT + c * 16);
+                        promote(g + c * 8, rg, cs + c * 16);
+                        promote(w + c * 8, ru, cs + NT + c * 16);
                     }
                 }
                 tc_fence_before();
@@ -971,7 +971,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                             uint32_t r[16];
                             tmem_ld16(tb + c * 16, r);
                             tmem_ld_wait();
-                            promote16(acc + c * 8, r, cs + c * 16);
+                            promote(acc + c * 8, r, cs + c * 16);
                         }
                     }
                     tc_fence_before();
