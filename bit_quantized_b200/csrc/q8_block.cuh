@@ -55,12 +55,28 @@ __device__ __forceinline__ void widen2(uint32_t u, float& a, float& b, __half) {
     b = f.y;
 }
 
+// Largest magnitude of 8 16-bit values, two at a time (exact: a maximum rounds
+// nothing).
+__device__ __forceinline__ float pair_max(__nv_bfloat162 a) { return fmaxf(__low2float(a), __high2float(a)); }
+__device__ __forceinline__ float pair_max(__half2 a) { return fmaxf(__low2float(a), __high2float(a)); }
+
+template <typename T2>
+__device__ __forceinline__ float absmax8_pairs(uint4 u) {
+    const uint32_t w[4] = {u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu, u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu};
+    const T2* h = reinterpret_cast<const T2*>(w);
+    return pair_max(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+}
+
+__device__ __forceinline__ float absmax8_16(uint4 u, __nv_bfloat16) { return absmax8_pairs<__nv_bfloat162>(u); }
+__device__ __forceinline__ float absmax8_16(uint4 u, __half) { return absmax8_pairs<__half2>(u); }
+
 // 8 consecutive values as fp32, from a 16-byte-aligned address.
 template <typename T>
 struct Eight {
     uint4 u;
     __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float absmax() const { return absmax8_16(u, T()); }
     __device__ __forceinline__ void values(float (&f)[8]) const {
         widen2(u.x, f[0], f[1], T());
         widen2(u.y, f[2], f[3], T());
@@ -77,6 +93,10 @@ struct Eight<float> {
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float absmax() const {
+        return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                     fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+    }
     __device__ __forceinline__ void values(float (&f)[8]) const {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -89,13 +109,6 @@ __device__ __forceinline__ float ldg_volatile(const float* p) {
     return v;
 }
 
-__device__ __forceinline__ float absmax8(const float (&f)[8]) {
-    float m = fabsf(f[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-    return m;
-}
-
 // One quantization group spread over 8 lanes (16 values each): codes of this
 // lane's 16 values and the group's scale.
 template <typename T>
@@ -103,7 +116,7 @@ __device__ __forceinline__ uint4 quantize16(const Eight<T>& lo, const Eight<T>& 
     float a[8], b[8];
     lo.values(a);
     hi.values(b);
-    float m = fmaxf(absmax8(a), absmax8(b));
+    float m = fmaxf(lo.absmax(), hi.absmax());
 #pragma unroll
     for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const BlockScale s = block_scale(m);

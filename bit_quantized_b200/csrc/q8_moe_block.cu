@@ -168,7 +168,7 @@ moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restri
         else v.zero();
         float f[8];
         v.values(f);
-        float a = absmax8(f);
+        float a = v.absmax();
 #pragma unroll
         for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         const BlockScale s = block_scale(a);
