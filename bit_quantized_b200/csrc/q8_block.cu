@@ -37,47 +37,58 @@ constexpr int kBKB = 128;   // bytes of K per stage: one scale group, one swizzl
 // the codes.  16 lanes share a group of 128 values (16 bytes of a 16-bit type
 // each).
 
+// Bytes in flight bound them: CTAs of 32 KB of input, four or five per SM
+// (4096x8192 bf16 activations: 21.4 us with 16 KB, 19.1 with 32 = 5.3 TB/s, 22.9
+// with 64; 8192x8192 bf16 weights: 38.3 us = 5.3 TB/s, with 64 KB 43.0; persistent
+// forms that load a tile ahead: 22.9 and 47.2; fp32: 6.1 and 6.3 TB/s).
 constexpr int kActRows = 32;   // rows per block: the scales of a group leave as one run
 
-// Activation: 32 rows x 256 columns (two groups) per block; a warp takes four
-// rows, 512 bytes of each.  What bounds it is the arithmetic, so the four rows'
-// maxima are reduced together, each lane ends with one row's and computes that
-// row's scale alone, and the scales go round by shuffles (4096x8192 bf16:
-// 21.4 us with a reduction and a scale per row and lane).  The scales are
-// group-major, so they are gathered in shared memory and written as runs of 32
-// rows.
-template <typename T>
+// Activation: 32 rows x 256 H columns per block; a warp takes four rows, H times
+// 512 bytes of each (H = 2 for 16-bit inputs: 32 KB per block).  The 4 H maxima
+// of a lane are reduced together: lanes 8, 4 (and 2) apart split them, so that
+// each lane ends with one row's and computes that group's scale alone; the
+// scales go round by shuffles.  The scales are group-major, so they are
+// gathered in shared memory and written as runs of 32 rows.
+template <typename T, int H>
 __global__ void __launch_bounds__(256)
 act_block_quant_kernel(const T* __restrict__ X, int64_t m, int64_t k, int64_t ldx, uint8_t* __restrict__ codes,
                        float* __restrict__ scale) {
-    __shared__ float s_sh[2][kActRows];
+    constexpr int N = 4 * H;                 // pieces: row i / H, columns i % H
+    __shared__ float s_sh[2 * H][kActRows];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kActRows + warp * 4;
-    const int64_t col = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.y) * (256 * H) + lane * 8;
     pdl_wait();
     pdl_launch_dependents();
-    Eight<T> v[4];
-    float a[4];
+    Eight<T> v[N];
+    float a[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (row0 + i < m && col < k) v[i].load(X + (row0 + i) * ldx + col);
+    for (int i = 0; i < N; ++i) {
+        const int64_t r = row0 + i / H, col = col0 + i % H * 256;
+        if (r < m && col < k) v[i].load(X + r * ldx + col);
         else v[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = v[i].absmax();
-    // 16 lanes, four rows: lanes 8 apart split the rows into pairs, lanes 4
-    // apart into single rows, then each row is reduced over its four lanes.
-    const bool up8 = lane & 8, up4 = lane & 4;
-    float b0 = fmaxf(up8 ? a[2] : a[0], __shfl_xor_sync(0xffffffffu, up8 ? a[0] : a[2], 8));
-    float b1 = fmaxf(up8 ? a[3] : a[1], __shfl_xor_sync(0xffffffffu, up8 ? a[1] : a[3], 8));
-    float c = fmaxf(up4 ? b1 : b0, __shfl_xor_sync(0xffffffffu, up4 ? b0 : b1, 4));
-    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 2));
-    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 1));
-    const BlockScale mine = block_scale(c);             // of row (lane / 4) % 4, group lane / 16
-    if (lane % 4 == 0) s_sh[lane / 16][warp * 4 + (lane / 4) % 4] = mine.S;
+    for (int i = 0; i < N; ++i) a[i] = v[i].absmax();
+    int left = N, mine_i = 0;                // this lane's piece
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int from = (lane & 16) + 4 * i;
+    for (int o = 8; o; o >>= 1) {
+        if (left > 1) {
+            const bool up = lane & o;
+            left /= 2;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < left) a[i] = fmaxf(up ? a[i + left] : a[i], __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + left], o));
+            if (up) mine_i += left;
+        } else {
+            a[0] = fmaxf(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+        }
+    }
+    const BlockScale mine = block_scale(a[0]);
+    if (lane % (16 / N) == 0) s_sh[mine_i % H * 2 + lane / 16][warp * 4 + mine_i / H] = mine.S;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int from = (lane & 16) + i * (16 / N);
         BlockScale s;
         s.S = __shfl_sync(0xffffffffu, mine.S, from);
         s.R = __shfl_sync(0xffffffffu, mine.R, from);
@@ -85,12 +96,13 @@ act_block_quant_kernel(const T* __restrict__ X, int64_t m, int64_t k, int64_t ld
         float f[8];
         v[i].values(f);
         const uint2 w = make_uint2(block_codes4(f[0], f[1], f[2], f[3], s), block_codes4(f[4], f[5], f[6], f[7], s));
-        if (row0 + i < m && col < k) *reinterpret_cast<uint2*>(codes + (row0 + i) * k + col) = w;
+        const int64_t r = row0 + i / H, col = col0 + i % H * 256;
+        if (r < m && col < k) *reinterpret_cast<uint2*>(codes + r * k + col) = w;
     }
     __syncthreads();
-    if (threadIdx.x < 2 * kActRows) {
+    if (threadIdx.x < 2 * H * kActRows) {
         const int g = threadIdx.x / kActRows, i = threadIdx.x % kActRows;
-        const int64_t j = static_cast<int64_t>(blockIdx.y) * 2 + g, r = static_cast<int64_t>(blockIdx.x) * kActRows + i;
+        const int64_t j = static_cast<int64_t>(blockIdx.y) * 2 * H + g, r = static_cast<int64_t>(blockIdx.x) * kActRows + i;
         if (j * kBlock < k && r < m) scale[j * m + r] = s_sh[g][i];
     }
 }
@@ -800,8 +812,9 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
 // ============================================================================
 template <typename T>
 cudaError_t act_quant(const BlockQuantArgs& a, cudaStream_t s) {
+    constexpr int H = sizeof(T) == 2 ? 2 : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kActRows - 1) / kActRows), static_cast<unsigned>((a.k + 255) / 256), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kActRows - 1) / kActRows), static_cast<unsigned>((a.k + 256 * H - 1) / (256 * H)), 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -809,7 +822,7 @@ cudaError_t act_quant(const BlockQuantArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, act_block_quant_kernel<T>, static_cast<const T*>(a.src), a.rows, a.k, a.ld,
+    return cudaLaunchKernelEx(&cfg, act_block_quant_kernel<T, H>, static_cast<const T*>(a.src), a.rows, a.k, a.ld,
                               static_cast<uint8_t*>(a.codes), a.scale);
 }
 
