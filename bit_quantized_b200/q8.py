@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -515,9 +516,9 @@ def q8_linear_fp8_grouped(x: QAct, w: QWeight, num_experts: int, offsets: torch.
 # ---------------------------------------------------------------- block-scaled FP8
 #
 # These calls run on the device of their first tensor (made current for the
-# call) and on that device's current torch stream unless `stream` names
-# another.  Outputs and workspaces allocated here for another stream are
-# recorded on it, so that their memory is not reused under the kernels.
+# call) and on that device's current torch stream.  With `stream` the whole
+# call, its allocations included, runs in that stream's context, so that what it
+# returns belongs to that stream, as with any torch operation there.
 
 @dataclasses.dataclass
 class QWeightBlock:
@@ -562,33 +563,30 @@ class QActBlock:
         want = ((k + 127) // 128, m)
         if S.device != q.device or S.dtype is not torch.float32 or S.shape != want or not S.is_contiguous():
             raise ValueError(f"activation scale must be a contiguous float32 tensor of shape {want} on the codes' device")
-        return CActBlock(q.data_ptr(), S.data_ptr(), m, k, q.stride(0))
+        return CActBlock(q.data_ptr(), S.data_ptr(), m, k, _ld(q))
 
 
-def _on(device, call, made, stream, where, args, others=()):
-    """Runs a C entry point with `device` current, on its stream; `made` tensors were allocated for the call."""
+def _in_stream(stream, device, fn, *args, **kwargs):
+    """fn in the context of a stream of the tensors' device."""
+    if stream.device != device:
+        raise ValueError(f"the stream must belong to {device}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kwargs)
+
+
+def _launch(device, call, where, args, others=()):
+    """Runs a C entry point with `device` current, on its current stream."""
     for t, name in others:
         if t is not None and t.device != device:
             raise ValueError(f"{name} must be on {device}")
     index = device.index
-    if index != torch._C._cuda_getDevice():
+    if index == torch._C._cuda_getDevice():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
         with torch.cuda.device(index):
-            return _launch(index, call, made, stream, where, args)
-    return _launch(index, call, made, stream, where, args)
-
-
-def _launch(index, call, made, stream, where, args):
-    raw = torch._C._cuda_getCurrentRawStream(index)
-    if stream is None or stream.cuda_stream == raw:
-        status = call(*args, raw)
-        if status:
-            raise Q8Error(status, where)
-        return
-    if stream.device_index != index:
-        raise ValueError(f"the stream must belong to cuda:{index}")
-    _check(call(*args, stream.cuda_stream), where)
-    for t in made:
-        t.record_stream(stream)
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        raise Q8Error(status, where)
 
 
 def _check_out(out, shape, dtype, device, name="out"):
@@ -599,6 +597,14 @@ def _check_out(out, shape, dtype, device, name="out"):
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _bytes(workspace: Optional[torch.Tensor]) -> int:
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -615,25 +621,27 @@ def _check_bias(bias, n, device):
 
 def q8_quantize_act_block(X: torch.Tensor, out: Optional[QActBlock] = None, stream=None) -> QActBlock:
     """FP8 codes with one scale per token and 128 values (see q8_quantize_act_block in q8.h)."""
+    if stream is not None:
+        return _in_stream(stream, X.device, q8_quantize_act_block, X, out)
     _cuda(X, "X")
     m, k = X.shape
-    made = ()
     if out is None:
         out = QActBlock(torch.empty((m, k), dtype=torch.float8_e4m3fn, device=X.device),
                         torch.empty(((k + 127) // 128, m), dtype=torch.float32, device=X.device))
-        made = (out.codes, out.scale)
     else:
         out.c()
         _check_out(out.codes, (m, k), torch.float8_e4m3fn, X.device, "out.codes")
         if not out.codes.is_contiguous():
             raise ValueError("out.codes must be contiguous")
-    _on(X.device, _lib.q8_quantize_act_block, made, stream, "q8_quantize_act_block",
+    _launch(X.device, _lib.q8_quantize_act_block, "q8_quantize_act_block",
         (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, k, _ld(X), out.codes.data_ptr(), out.scale.data_ptr()))
     return out
 
 
 def q8_quantize_weight_block(W: torch.Tensor, stream=None) -> QWeightBlock:
     """FP8 codes with one scale per 128 x 128 block; W is n x k, or a stack experts x n x k."""
+    if stream is not None:
+        return _in_stream(stream, W.device, q8_quantize_weight_block, W)
     stack = W.dim() == 3
     if stack and not W.is_contiguous():
         raise ValueError("a stack of weights must be contiguous")
@@ -643,7 +651,7 @@ def q8_quantize_weight_block(W: torch.Tensor, stream=None) -> QWeightBlock:
     shape = (((n + 127) // 128), (k + 127) // 128)
     q = torch.empty(W.shape, dtype=torch.float8_e4m3fn, device=W.device)
     S = torch.empty((e, *shape) if stack else shape, dtype=torch.float32, device=W.device)
-    _on(W.device, _lib.q8_quantize_weight_block, (q, S), stream, "q8_quantize_weight_block",
+    _launch(W.device, _lib.q8_quantize_weight_block, "q8_quantize_weight_block",
         (W2.data_ptr(), _FLOAT_DT.get(W.dtype, -1), e, n, k, _ld(W2), q.data_ptr(), S.data_ptr()))
     return QWeightBlock(q, S)
 
@@ -651,42 +659,44 @@ def q8_quantize_weight_block(W: torch.Tensor, stream=None) -> QWeightBlock:
 def q8_linear_fp8_block(x: QActBlock, w: QWeightBlock, bias: Optional[torch.Tensor] = None,
                         out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Block-scaled FP8 linear of a quantized activation; returns bf16 m x n."""
+    if stream is not None:
+        return _in_stream(stream, x.codes.device, q8_linear_fp8_block, x, w, bias, out)
     cx, cw = x.c(), w.c()
     dev = x.codes.device
-    made = ()
     if out is None:
         out = torch.empty((cx.m, cw.n), dtype=torch.bfloat16, device=dev)
-        made = (out,)
     else:
         _check_out(out, (cx.m, cw.n), torch.bfloat16, dev)
     _check_bias(bias, cw.n, dev)
-    _on(dev, _lib.q8_linear_fp8_block, made, stream, "q8_linear_fp8_block",
+    _launch(dev, _lib.q8_linear_fp8_block, "q8_linear_fp8_block",
         (ctypes.byref(cx), ctypes.byref(cw), _addr(bias), out.data_ptr(), _ld(out)), ((w.codes, "w"),))
     return out
+
+
+# Up to this many tokens q8_linear_fp8_block_dynamic needs no workspace.
+_FUSED_TOKENS = 16
 
 
 def q8_linear_fp8_block_dynamic(X: torch.Tensor, w: QWeightBlock, bias: Optional[torch.Tensor] = None,
                                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                                 stream=None) -> torch.Tensor:
     """Activation quantization and block-scaled FP8 linear in one call; returns bf16 m x n."""
+    if stream is not None:
+        return _in_stream(stream, X.device, q8_linear_fp8_block_dynamic, X, w, bias, out, workspace)
     _cuda(X, "X")
     m, k = X.shape
     cw = w.c()
     dev = X.device
-    made = []
     if out is None:
         out = torch.empty((m, cw.n), dtype=torch.bfloat16, device=dev)
-        made.append(out)
     else:
         _check_out(out, (m, cw.n), torch.bfloat16, dev)
-    need = q8_workspace_size(Q8_OP_LINEAR_FP8_BLOCK, m, cw.n, k)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        made.append(workspace)
+    if workspace is None and m > _FUSED_TOKENS:
+        workspace = torch.empty(q8_workspace_size(Q8_OP_LINEAR_FP8_BLOCK, m, cw.n, k), dtype=torch.uint8, device=dev)
     _check_bias(bias, cw.n, dev)
-    _on(dev, _lib.q8_linear_fp8_block_dynamic, made, stream, "q8_linear_fp8_block_dynamic",
+    _launch(dev, _lib.q8_linear_fp8_block_dynamic, "q8_linear_fp8_block_dynamic",
         (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, k, _ld(X), ctypes.byref(cw), _addr(bias), out.data_ptr(), _ld(out),
-         _addr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()),
+         _addr(workspace), _bytes(workspace)),
         ((w.codes, "w"), (workspace, "workspace")))
     return out
 
@@ -696,20 +706,20 @@ def q8_linear_fp8_block_grouped(x: QActBlock, w: QWeightBlock, offsets: torch.Te
                                 stream=None) -> torch.Tensor:
     """Grouped block-scaled FP8 linear (mixture of experts): tokens sorted by expert, w a stack of
     experts, offsets a CUDA int32 tensor of experts + 1 entries; returns bf16 m x n."""
+    if stream is not None:
+        return _in_stream(stream, x.codes.device, q8_linear_fp8_block_grouped, x, w, offsets, bias, out)
     cx, cw = x.c(), w.c()
     e = w.experts
     dev = x.codes.device
     if offsets.device != dev or offsets.dtype != torch.int32 or offsets.shape != (e + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets must be a contiguous int32 tensor of {e + 1} entries on {dev}")
     n = cw.n // max(e, 1)
-    made = ()
     if out is None:
         out = torch.empty((cx.m, n), dtype=torch.bfloat16, device=dev)
-        made = (out,)
     else:
         _check_out(out, (cx.m, n), torch.bfloat16, dev)
     _check_bias(bias, cw.n, dev)
-    _on(dev, _lib.q8_linear_fp8_block_grouped, made, stream, "q8_linear_fp8_block_grouped",
+    _launch(dev, _lib.q8_linear_fp8_block_grouped, "q8_linear_fp8_block_grouped",
         (ctypes.byref(cx), ctypes.byref(cw), e, offsets.data_ptr(), _addr(bias), out.data_ptr(), _ld(out)),
         ((w.codes, "w"),))
     return out
@@ -721,16 +731,17 @@ _SCORING = {"softmax": Q8_SOFTMAX, "sigmoid": Q8_SIGMOID}
 def q8_moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", renormalize: bool = True,
                  out=None, stream=None):
     """The router's top-k choice (see q8_moe_route in q8.h): (ids int32 m x top_k, weights fp32 m x top_k)."""
+    if stream is not None:
+        return _in_stream(stream, logits.device, q8_moe_route, logits, top_k, scoring, renormalize, out)
     _cuda(logits, "logits")
     m, experts = logits.shape
     dev = logits.device
-    made = ()
     if out is None:
-        out = made = (torch.empty((m, top_k), dtype=torch.int32, device=dev),
-                      torch.empty((m, top_k), dtype=torch.float32, device=dev))
+        out = (torch.empty((m, top_k), dtype=torch.int32, device=dev),
+               torch.empty((m, top_k), dtype=torch.float32, device=dev))
     ids, weights = out
     _check_choice(ids, weights, m, top_k, dev)
-    _on(dev, _lib.q8_moe_route, made, stream, "q8_moe_route",
+    _launch(dev, _lib.q8_moe_route, "q8_moe_route",
         (logits.data_ptr(), _FLOAT_DT.get(logits.dtype, -1), m, experts, _ld(logits), top_k,
          _SCORING.get(scoring, -1), int(renormalize), ids.data_ptr(), weights.data_ptr()))
     return ids, weights
@@ -743,6 +754,7 @@ def _check_choice(ids, weights, m, top_k, device):
         raise ValueError(f"ids and weights must be contiguous int32 and float32 tensors of shape {(m, top_k)} on {device}")
 
 
+@functools.lru_cache(maxsize=1024)
 def q8_moe_workspace_size(m: int, top_k: int, num_experts: int, hidden: int, inter: int) -> int:
     return int(_lib.q8_moe_workspace_size(m, top_k, num_experts, hidden, inter))
 
@@ -753,6 +765,8 @@ def q8_moe_fp8_block(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
     """The whole expert layer for up to 64 tokens: w13 a stack experts x 2 inter x hidden (gate rows,
     then up rows), w2 a stack experts x hidden x inter, ids and weights as q8_moe_route gives them;
     returns bf16 m x hidden."""
+    if stream is not None:
+        return _in_stream(stream, X.device, q8_moe_fp8_block, X, ids, weights, w13, w2, out, workspace)
     _cuda(X, "X")
     m, hidden = X.shape
     dev = X.device
@@ -762,20 +776,17 @@ def q8_moe_fp8_block(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, 
         raise ValueError("w13 and w2 must hold the same number of experts")
     top_k = ids.shape[1] if ids.dim() == 2 else 0
     _check_choice(ids, weights, m, top_k, dev)
-    made = []
     if out is None:
         out = torch.empty((m, hidden), dtype=torch.bfloat16, device=dev)
-        made.append(out)
     else:
         _check_out(out, (m, hidden), torch.bfloat16, dev)
     if workspace is None:
         need = q8_moe_workspace_size(m, top_k, experts, hidden, c2.k)
         workspace = torch.empty(need if need < 1 << 62 else 0, dtype=torch.uint8, device=dev)
-        made.append(workspace)
-    _on(dev, _lib.q8_moe_fp8_block, made, stream, "q8_moe_fp8_block",
+    _launch(dev, _lib.q8_moe_fp8_block, "q8_moe_fp8_block",
         (X.data_ptr(), _FLOAT_DT.get(X.dtype, -1), m, hidden, _ld(X), ids.data_ptr(), weights.data_ptr(), top_k,
          ctypes.byref(c13), ctypes.byref(c2), experts, out.data_ptr(), _ld(out), _addr(workspace),
-         workspace.numel() * workspace.element_size()),
+         _bytes(workspace)),
         ((w13.codes, "w13"), (w2.codes, "w2"), (workspace, "workspace")))
     return out
 
