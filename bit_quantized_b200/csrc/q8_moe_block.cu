@@ -594,7 +594,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 if (finish) {
                     // Four contributors' sums of two tokens are asked for together.
                     auto part = [&](int c) {
-                        return p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > u * p.kb1 ? 0 : 1)) * (2 * NT * kBM) + ch;
+                        return p.part + (static_cast<int64_t>(c) * 2 + (c > first ? 0 : 1)) * (2 * NT * kBM) + ch;
                     };
 #pragma unroll 1
                     for (int i = 0; i < cn; i += 2) {
@@ -744,7 +744,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     // per warp: the sums over experts, or those of all contributors in the order
     // of the CTAs.
     auto sum_tile = [&](int nt, int first, int lastc) {
-        const int n = nt * kBM + lane * 4, tile0 = nt * tile_steps;
+        const int n = nt * kBM + lane * 4;
 #pragma unroll 1
         for (int t = warp - 2; t < p.m; t += 8 * C::SUM_TOKENS) {
             float4 v[C::SUM_TOKENS];
@@ -757,7 +757,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             if (first != lastc) {
 #pragma unroll 4
                 for (int c = first; c <= lastc; ++c) {
-                    const float* src = p.part + (static_cast<int64_t>(c) * 2 + (line.start(c) > tile0 ? 0 : 1)) * (p.m * kBM) + lane * 4;
+                    const float* src = p.part + (static_cast<int64_t>(c) * 2 + (c > first ? 0 : 1)) * (p.m * kBM) + lane * 4;
 #pragma unroll
                     for (int j = 0; j < C::SUM_TOKENS; ++j) {
                         const float4 x = __ldcg(reinterpret_cast<const float4*>(src + min(t + 8 * j, p.m - 1) * kBM));
