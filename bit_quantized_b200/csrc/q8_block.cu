@@ -189,10 +189,12 @@ struct BlockTileCfg {
     static constexpr int STORE = kPromoWarps * 2048;       // output staging: one 32 x 32 chunk per warp
     static constexpr int STAGES_RAW = (227 * 1024 - STORE - 1024 - 6 * 1024) / STAGE;
     static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
-    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int TMEM_COLS = BN <= 128 ? 256 : 512;
     static constexpr int CW = BN / 2;                      // columns per promotion warp
+    // 96 columns may reach into a second weight block (at a multiple of 32).
+    static constexpr bool TWO = CW % 128 != 0 && 128 % CW != 0;
     static constexpr int SMEM = STAGES * STAGE + STORE + 1024;
-    static_assert(BN == 128 || BN == 256, "a warp's columns lie in one weight block");
+    static_assert(BN == 128 || BN == 192 || BN == 256, "BN");
 };
 
 template <int BN, bool GROUPED>
@@ -366,6 +368,8 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             const int e = GROUPED ? tr.col_off / p.n : 0;
             const float* sx = p.sx + (row < p.m ? row : p.m - 1);
             const float* sw = p.sw + (static_cast<int64_t>(e) * nb_all + nb) * num_kb;
+            const int64_t to_next = nb + 1 < nb_all ? num_kb : 0;   // the next block's scales
+            const int cut = (ncol / kBlock + 1) * kBlock - ncol;    // columns before it
             float2 acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -373,11 +377,15 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             // volatile and the products are formed at the use: left to itself,
             // the compiler forms them right behind the loads, and every fourth
             // group then waits about 2000 cycles for memory.
-            float s_a[4], s_b[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            float s_a[4], s_b[4], s_c[C::TWO ? 4 : 1];
+            auto fetch = [&](int j) {
                 s_a[j] = ldg_volatile(sx);
                 s_b[j] = ldg_volatile(sw);
+                if constexpr (C::TWO) s_c[j] = ldg_volatile(sw + to_next);
+            };
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                fetch(j);
                 if (j + 1 < num_kb) {              // past the end: loaded again, not used
                     sx += p.m;
                     ++sw;
@@ -395,6 +403,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     __syncwarp();
                     tc_fence_after();
                     const float sc = s_a[j] * s_b[j];
+                    const float sc2 = C::TWO ? s_a[j] * s_c[C::TWO ? j : 0] : sc;
                     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + half * C::CW;
 #pragma unroll
                     for (int c = 0; c < C::CW / 32; ++c) {
@@ -407,10 +416,9 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&tempty_bar[buf]);
                         }
-                        promote(acc + c * 16, r, sc);
+                        promote(acc + c * 16, r, C::TWO && c * 32 >= cut ? sc2 : sc);
                     }
-                    s_a[j] = ldg_volatile(sx);
-                    s_b[j] = ldg_volatile(sw);
+                    fetch(j);
                     if (kb + 5 < num_kb) {
                         sx += p.m;
                         ++sw;
@@ -513,7 +521,6 @@ struct BlockDecodeCfg {
     static constexpr int PROMO = 4 * SETS;
     static constexpr int THREADS = 32 * (2 + PROMO + (QX ? kQxWarps : 0));
     static constexpr int CW = NT / HALVES;       // columns per promotion warp
-    static constexpr int QUADS = NT / 4;
     static constexpr int A_BYTES = kBM * kBKB;   // 128 weight rows
     static constexpr int B_BYTES = NT * kBKB;    // NT token rows
     static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -937,16 +944,18 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
 }
 
 // Tile width: the persistent grid's makespan, waves x (BN + a tile's fixed cost
-// of about 64 columns' worth), the narrower tile on ties (16 experts x 2048 x
-// 4096, 4096 tokens: 65 us with 128 columns, 74 with 256; 1024x4096x4096: 26.6
-// and 18.9, 2048x14336x4096: 150 and 142).
-bool wide_tiles(int64_t row_tiles, int64_t n) {
+// of about 64 columns' worth), the narrower tile on ties.
+template <bool GROUPED>
+q8_status run_tiles(const BlockLinearArgs& a, int64_t row_tiles, cudaStream_t s) {
     const int64_t sms = sm_count();
     auto cost = [&](int64_t bn) {
-        const int64_t tiles = row_tiles * ((n + bn - 1) / bn);
+        const int64_t tiles = row_tiles * ((a.n + bn - 1) / bn);
         return ((tiles + sms - 1) / sms) * (bn + 64);
     };
-    return cost(256) < cost(128);
+    const int64_t narrow = cost(128), middle = cost(192), wide = cost(256);
+    if (wide < middle && wide < narrow) return run_block_tile<256, GROUPED>(a, s);
+    if (middle < narrow) return run_block_tile<192, GROUPED>(a, s);
+    return run_block_tile<128, GROUPED>(a, s);
 }
 
 }  // namespace
@@ -965,7 +974,7 @@ q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
         // full ones, and one for every expert where they average fewer rows.
         const int64_t full = (a.m + kBM - 1) / kBM, some = a.experts < a.m ? a.experts : a.m;
         const int64_t rows = full + a.experts / 2 > some ? full + a.experts / 2 : some;
-        return wide_tiles(rows, a.n) ? run_block_tile<256, true>(a, s) : run_block_tile<128, true>(a, s);
+        return run_tiles<true>(a, rows, s);
     }
     if (a.x) {   // quantized on the way
         switch (a.x_dtype) {
@@ -978,7 +987,7 @@ q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     if (a.m <= 32) return run_block_decode<32, false, __half>(a, s);
     if (a.m <= 64) return run_block_decode<64, false, __half>(a, s);
     if (a.m <= 2 * kBM) return run_block_decode<128, false, __half>(a, s);
-    return wide_tiles((a.m + kBM - 1) / kBM, a.n) ? run_block_tile<256, false>(a, s) : run_block_tile<128, false>(a, s);
+    return run_tiles<false>(a, (a.m + kBM - 1) / kBM, s);
 }
 
 }  // namespace q8

@@ -332,9 +332,12 @@ struct MoeUpCfg {
     static constexpr int THREADS = 32 * (2 + 8);
     static constexpr int B_BYTES = NT * kBKB;
     static constexpr int STAGE = 2 * kBM * kBKB + B_BYTES;
-    // Up to 32 tokens two CTAs fit an SM, so that the down projection's can
-    // take their place and ask for their weights while this kernel ends.
-    static constexpr int STAGES = NT <= 32 ? 3 : 4;
+    // About 100 KB of weights on their way per SM: a longer ring streams no
+    // faster and only delays what waits behind it, the sums that contributors
+    // exchange.  Up to 32 tokens two CTAs then fit an SM, so that the down
+    // projection's can take their place and ask for their weights while this
+    // kernel ends.
+    static constexpr int STAGES = 3;
     static constexpr int TMEM_COLS = 8 * NT;
     static constexpr int SMEM = STAGES * STAGE + 1024;
 };
@@ -679,10 +682,10 @@ struct MoeDownCfg {
     static constexpr int B_BYTES = NT * kBKB;
     static constexpr int STAGE = kBM * kBKB + B_BYTES;
     static constexpr int OUT = NT * kBM * 4;          // the tile's sums over experts
-    static constexpr int MAX_STAGES = NT <= 32 ? 9 : 7;
+    static constexpr int MAX_STAGES = NT <= 32 ? 7 : 5;
     // Few steps: a ring that fits an SM beside a CTA of the up projection, so
     // that the first weights are on their way while that one ends.
-    static constexpr int FEW_STAGES = NT <= 16 ? 5 : NT <= 32 ? 4 : 7;
+    static constexpr int FEW_STAGES = NT <= 16 ? 5 : NT <= 32 ? 4 : 5;
     static constexpr int TMEM_COLS = 2 * NT;
     static constexpr int SUM_TOKENS = 4;              // tokens a warp sums at a time
     static constexpr int smem(int stages) { return stages * STAGE + OUT + 1024; }
