@@ -528,6 +528,7 @@ struct BlockDecodeCfg {
     // Scales of groups quantized on the way: a stage is refilled when its MMA
     // is done, with the promotion at most four groups behind the MMA.
     static constexpr int SX_RING = MAX_STAGES + 4;
+    static constexpr int STATIC = 4 * 1024 + (QX ? 0 : PROMO * kScaleRing * CW * 4);   // static shared memory, at most
     static constexpr int TMEM_COLS = 2 * TEAMS * NT;   // at least the 32 an allocation takes
     static_assert(!QX || NT == 16, "the quantizing warps cover 16 tokens");
 };
@@ -549,6 +550,8 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     __shared__ __align__(16) float col_s[C::PROMO][C::CW];         // promotion warps: Sx Sw of the group
+    __shared__ float sxa_ring[QX ? 1 : C::PROMO][QX ? 1 : kScaleRing][QX ? 1 : C::CW];
+    __shared__ float sw_ring[C::PROMO][kScaleRing];
     __shared__ float sx_ring[QX ? C::SX_RING : 1][QX ? NT : 1];
     __shared__ __align__(8) uint64_t sx_bar[QX ? C::SX_RING : 1];  // every quad of the slot is written
 
@@ -679,33 +682,42 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         float2 acc[C::CW / 2];
 #pragma unroll
         for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-        constexpr int NS = (C::CW + 31) / 32;           // column scales per lane
-        float sxv[NS], swk = team < my_kb ? __ldg(sw + team) : 0.f;
-        auto fetch_sx = [&](int i) {
-#pragma unroll
-            for (int c = 0; c < NS; ++c) {
-                const int t = c * 32 + lane;
-                sxv[c] = t < cn ? __ldg(p.sx + static_cast<int64_t>(kb0 + i) * p.m + t0 + c0 + t) : 0.f;
-            }
+        // The scales of a group are asked for kAhead of the team's groups before
+        // their use, by asynchronous copies into a ring of each warp.
+        const int groups = my_kb > team ? (my_kb - team + C::TEAMS - 1) / C::TEAMS : 0;   // of this team
+        auto ask_sw = [&](int n) {
+            if (n < groups && lane == 0) cp_async4(&sw_ring[warp - 2][n % kScaleRing], sw + team + n * C::TEAMS);
         };
-        if constexpr (!QX) {
-            pdl_wait();
-            if (team < my_kb) fetch_sx(team);
-        }
-        for (int i = team; i < my_kb; i += C::TEAMS) {
-            const int n = i / C::TEAMS, buf = team * 2 + (n & 1);
+        auto ask_sx = [&](int n) {
+            if constexpr (!QX) {
+                if (n < groups) {
+#pragma unroll
+                    for (int c = 0; c < C::CW; c += 32)
+                        if (c + lane < cn)
+                            cp_async4(&sxa_ring[warp - 2][n % kScaleRing][c + lane],
+                                      p.sx + static_cast<int64_t>(kb0 + team + n * C::TEAMS) * p.m + t0 + c0 + c + lane);
+                }
+            }
+            cp_async_commit();
+        };
+        for (int n = 0; n < kAhead; ++n) ask_sw(n);     // weights do not depend on the previous kernel
+        if constexpr (!QX) pdl_wait();
+        for (int n = 0; n < kAhead; ++n) ask_sx(n);
+        for (int n = 0; n < groups; ++n) {
+            const int i = team + n * C::TEAMS, buf = team * 2 + (n & 1), slot = n % kScaleRing;
+            ask_sw(n + kAhead);
+            ask_sx(n + kAhead);
+            cp_async_wait<kAhead>();
+            __syncwarp();
+            const float swk = sw_ring[warp - 2][slot];
             if constexpr (QX) {
                 if (!mbar_wait_short(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
                 if (lane < C::CW) cs[lane] = lane < cn ? sx_ring[i % C::SX_RING][lane] * swk : 0.f;
             } else {
 #pragma unroll
-                for (int c = 0; c < NS; ++c) {
-                    const int t = c * 32 + lane;
-                    if (t < C::CW) cs[t] = sxv[c] * swk;
-                }
-                if (i + C::TEAMS < my_kb) fetch_sx(i + C::TEAMS);
+                for (int c = 0; c < C::CW; c += 32)
+                    if (c + lane < C::CW) cs[c + lane] = c + lane < cn ? sxa_ring[warp - 2][slot][c + lane] * swk : 0.f;
             }
-            if (i + C::TEAMS < my_kb) swk = __ldg(sw + i + C::TEAMS);
             if (!mbar_wait_short(&tfull_bar[buf], (n >> 1) & 1, &abort_sh, p.status)) break;
             __syncwarp();
             tc_fence_after();
@@ -914,7 +926,7 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
     const int splits = (num_kb + per - 1) / per;
     const int quads = ((a.m < NT ? static_cast<int>(a.m) : NT) + 3) / 4;
     const int red = splits * C::TEAMS * ((quads + splits - 1) / splits) * kBM * 16;
-    const int budget = (tiles_n * tiles_t * splits > sm_count() ? 113 : 220) * 1024 - 4 * 1024 - red;
+    const int budget = (tiles_n * tiles_t * splits > sm_count() ? 113 : 222) * 1024 - C::STATIC - red;
     int nstages = budget / C::STAGE;
     if (nstages > C::MAX_STAGES) nstages = C::MAX_STAGES;
     if (nstages > per) nstages = per;

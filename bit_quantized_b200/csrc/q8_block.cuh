@@ -17,6 +17,11 @@ namespace {
 
 constexpr int kBlock = 128;   // values per scale along K, rows per weight scale
 
+// Where K groups are short, their scales are asked for kAhead groups before
+// their use, by asynchronous copies into a ring of each promotion warp (a
+// weight's scale comes from memory, and a group takes a few hundred cycles).
+constexpr int kAhead = 6, kScaleRing = 8;
+
 struct BlockScale {
     float S, R, Rlo;
 };

@@ -301,11 +301,6 @@ __device__ __forceinline__ void copy_list(ListSh& l, uint8_t* token_sh, const Mo
     __syncthreads();
 }
 
-// The scales of a step are asked for kAhead steps before their use, across tile
-// and expert borders, by asynchronous copies into a ring of each promotion warp
-// (a weight's scale comes from memory, and a step is only a few hundred cycles).
-constexpr int kAhead = 6, kScaleRing = 8;
-
 // Counts this CTA's arrival at a tile with `parts` contributors; true in the
 // one that arrives last, which then sees every contributor's sums.  Called by
 // 128 threads after each wrote its sums; the leader's fences cover them all
