@@ -657,7 +657,6 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                     for (int ks = 0; ks < kBKB / 32; ++ks)
                         mma_issue<kKindF8>(tmem_base + buf * NT, ad + 2 * ks, bd + 2 * ks, idesc, ks != 0);
                     tc_commit(&tfull_bar[buf]);
-                    tc_commit(&empty_bar[stage]);
                 }
                 __syncwarp();
                 if (++stage == nstages) {
@@ -720,6 +719,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             }
             if (!mbar_wait_short(&tfull_bar[buf], (n >> 1) & 1, &abort_sh, p.status)) break;
             __syncwarp();
+            if (warp - 2 == team * 4 && lane == 0) mbar_arrive(&empty_bar[i % nstages]);   // the MMAs have read the stage
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT + c0;
             constexpr int LW = C::CW >= 32 ? 32 : 16;   // columns per TMEM load
