@@ -51,7 +51,7 @@ constexpr int kActRows = 32;   // rows per block: the scales of a group leave as
 // gathered in shared memory and written as runs of 32 rows.
 template <typename T, int H>
 __global__ void __launch_bounds__(256)
-act_block_quant_kernel(const T* __restrict__ X, int64_t m, int64_t k, int64_t ldx, uint8_t* __restrict__ codes,
+act_block_quant_kernel(const T* X, int64_t m, int64_t k, int64_t ldx, uint8_t* __restrict__ codes,
                        float* __restrict__ scale) {
     constexpr int N = 4 * H;                 // pieces: row i / H, columns i % H
     __shared__ float s_sh[2 * H][kActRows];
@@ -389,9 +389,9 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             // group then waits about 2000 cycles for memory.
             float s_a[4], s_b[4], s_c[C::TWO ? 4 : 1];
             auto fetch = [&](int j) {
-                s_a[j] = ldg_volatile(sx);
-                s_b[j] = ldg_volatile(sw);
-                if constexpr (C::TWO) s_c[j] = ldg_volatile(sw + to_next);
+                s_a[j] = ld_scale(sx);
+                s_b[j] = ld_scale(sw);
+                if constexpr (C::TWO) s_c[j] = ld_scale(sw + to_next);
             };
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -423,8 +423,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                         if (c + 1 == C::CW / 32) {
                             // All of this warp's part is in registers: the buffer may be written again.
                             tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                            if (lane == 0) mbar_arrive_relaxed(&tempty_bar[buf]);
                         }
                         promote(acc + c * 16, r, C::TWO && c * 32 >= cut ? sc2 : sc);
                     }
@@ -546,7 +545,7 @@ struct BlockDecodeCfg {
 template <int NT, bool QX, typename T>
 __global__ void __launch_bounds__(BlockDecodeCfg<NT, QX>::THREADS, 1)
 gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                         const T* __restrict__ X, int64_t ldx, int k, const BlockParams p, int num_kb,
+                         const T* X, int64_t ldx, int k, const BlockParams p, int num_kb,
                          int kb_per_split, int splits, int nstages) {
     using C = BlockDecodeCfg<NT, QX>;
     extern __shared__ uint8_t smem_raw[];
@@ -888,6 +887,17 @@ q8_status run_block_tile(const BlockLinearArgs& a, cudaStream_t s) {
     if (!use_tmy) tY = tA;
     auto kern = gemm_block_tile_kernel<BN, GROUPED>;
     if (set_smem(kern, C::SMEM) != cudaSuccess) return Q8_ERR_LAUNCH;
+    // The warpgroups' register shares come out of what the block launches with:
+    // a build that launches with fewer would wait for ever.
+    static const bool registers_fit = [&] {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, kern) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return at.numRegs * kTileThreads >= 128 * kTileRegsLow + 256 * kTileRegsHigh;
+    }();
+    if (!registers_fit) return Q8_ERR_LAUNCH;
     const int tiles_n = static_cast<int>((a.n + BN - 1) / BN);
     const int tiles_m = static_cast<int>((a.m + kBM - 1) / kBM);
     // Grouped: an upper bound (each expert adds at most one partial row tile);
@@ -925,9 +935,10 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
     const int tiles_t = static_cast<int>((a.m + NT - 1) / NT);
     const int num_kb = static_cast<int>((a.k + kBKB - 1) / kBKB);
     // Split K across the CTAs of a cluster (at most 8, every split non-empty)
-    // as far as one wave holds: two CTAs per SM up to 32 tokens (a short stage
-    // ring), else one, and about 128 SMs where clusters of four and eight fit.
-    const int per_sm = NT <= 32 ? 2 : 1;
+    // as far as one wave holds: two CTAs per SM up to 16 tokens (a short stage
+    // ring; with more the registers allow one), and about 128 SMs where clusters
+    // of four and eight fit.
+    const int per_sm = NT == 16 ? 2 : 1;
     int want = 128 * per_sm / (tiles_n * tiles_t);
     if (want < 1) want = 1;
     if (want > 8) want = 8;
@@ -936,7 +947,7 @@ q8_status run_block_decode(const BlockLinearArgs& a, cudaStream_t s) {
     const int splits = (num_kb + per - 1) / per;
     const int quads = ((a.m < NT ? static_cast<int>(a.m) : NT) + 3) / 4;
     const int red = splits * C::TEAMS * ((quads + splits - 1) / splits) * kBM * 16;
-    const int budget = (tiles_n * tiles_t * splits > sm_count() ? 113 : 222) * 1024 - C::STATIC - red;
+    const int budget = (NT == 16 && static_cast<int64_t>(tiles_n) * splits > sm_count() ? 113 : 222) * 1024 - C::STATIC - red;
     int nstages = budget / C::STAGE;
     if (nstages > C::MAX_STAGES) nstages = C::MAX_STAGES;
     if (nstages > per) nstages = per;
@@ -1008,7 +1019,12 @@ q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     if (a.m <= 16) return run_block_decode<16, false, __half>(a, s);
     if (a.m <= 32) return run_block_decode<32, false, __half>(a, s);
     if (a.m <= 64) return run_block_decode<64, false, __half>(a, s);
-    if (a.m <= 2 * kBM) return run_block_decode<128, false, __half>(a, s);
+    // Up to 256 tokens as long as K can be split at least four ways in one wave;
+    // with more output the tile kernel's larger tiles are faster (256x4096x4096:
+    // 15.3 us split, 12.9 in tiles; 128x4096x4096: 10.1 and 12.3; 200x14336x4096:
+    // 49 and 25).
+    if (a.m <= 2 * kBM && (a.m + kBM - 1) / kBM * ((a.n + kBM - 1) / kBM) <= 32)
+        return run_block_decode<128, false, __half>(a, s);
     return run_tiles<false>(a, (a.m + kBM - 1) / kBM, s);
 }
 

@@ -75,11 +75,13 @@ __device__ __forceinline__ float absmax8_pairs(uint4 u) {
 __device__ __forceinline__ float absmax8_16(uint4 u, __nv_bfloat16) { return absmax8_pairs<__nv_bfloat162>(u); }
 __device__ __forceinline__ float absmax8_16(uint4 u, __half) { return absmax8_pairs<__half2>(u); }
 
-// 8 consecutive values as fp32, from a 16-byte-aligned address.
+// 8 consecutive values as fp32, from a 16-byte-aligned address.  Plain loads:
+// with programmatic launch the previous kernel may write its output while this
+// one is already resident, so nothing it wrote is read as constant data.
 template <typename T>
 struct Eight {
     uint4 u;
-    __device__ __forceinline__ void load(const T* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ float absmax() const { return absmax8_16(u, T()); }
     __device__ __forceinline__ void values(float (&f)[8]) const {
@@ -94,8 +96,8 @@ template <>
 struct Eight<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ float absmax() const {
@@ -108,7 +110,13 @@ struct Eight<float> {
     }
 };
 
-__device__ __forceinline__ float ldg_volatile(const float* p) {
+// A scale of the tile kernel's promotion.  Volatile keeps it where it stands.
+// Non-coherent, because an ordinary load would be waited for by every barrier
+// operation that follows (4096x8192x8192: 295 us, with asynchronous copies 265,
+// so 248): it is issued after the programmatic-launch wait, no earlier read of
+// this kernel can have cached the line, and nothing writes the scales from then
+// on.
+__device__ __forceinline__ float ld_scale(const float* p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;

@@ -67,7 +67,7 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162f
 
 template <typename T>
 __global__ void __launch_bounds__(128)
-moe_route_kernel(const T* __restrict__ logits, int64_t ld, int64_t m, int experts, int top_k, int sigmoid,
+moe_route_kernel(const T* logits, int64_t ld, int64_t m, int experts, int top_k, int sigmoid,
                  int renormalize, int32_t* __restrict__ ids, float* __restrict__ weights) {
     const int lane = threadIdx.x % 32;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32;
@@ -152,8 +152,7 @@ struct MoeParams {
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-moe_prepare_kernel(const T* __restrict__ X, int64_t ldx, const int32_t* __restrict__ ids,
-                   const float* __restrict__ weights, const MoeParams p) {
+moe_prepare_kernel(const T* X, int64_t ldx, const int32_t* ids, const float* weights, const MoeParams p) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (blockIdx.x > 0) {
         // 256 columns (two groups) of eight tokens, a warp each.

@@ -618,6 +618,12 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0) if rows > 1 else max(t.stride(0), cols)
 
 
+def _one_weight(w: QWeightBlock):
+    if w.experts != 1:
+        raise ValueError("w is a stack of experts: use q8_linear_fp8_block_grouped")
+    return w.c()
+
+
 def _check_bias(bias, n, device):
     if bias is not None and (bias.device != device or bias.dtype != torch.float32 or bias.numel() != n
                              or not bias.is_contiguous()):
@@ -666,7 +672,7 @@ def q8_linear_fp8_block(x: QActBlock, w: QWeightBlock, bias: Optional[torch.Tens
     """Block-scaled FP8 linear of a quantized activation; returns bf16 m x n."""
     if stream is not None:
         return _in_stream(stream, x.codes.device, q8_linear_fp8_block, x, w, bias, out)
-    cx, cw = x.c(), w.c()
+    cx, cw = x.c(), _one_weight(w)
     dev = x.codes.device
     if out is None:
         out = _new(cx.m, cw.n, torch.bfloat16, dev)
@@ -690,7 +696,7 @@ def q8_linear_fp8_block_dynamic(X: torch.Tensor, w: QWeightBlock, bias: Optional
         return _in_stream(stream, X.device, q8_linear_fp8_block_dynamic, X, w, bias, out, workspace)
     _cuda(X, "X")
     m, k = X.shape
-    cw = w.c()
+    cw = _one_weight(w)
     dev = X.device
     if out is None:
         out = _new(m, cw.n, torch.bfloat16, dev)

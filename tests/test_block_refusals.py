@@ -142,3 +142,10 @@ def test_python_refusals():
                  lambda: q8.QActBlock(w.codes, w.scale).c(), lambda: q8.q8_moe_fp8_block(X, X, X, w, w)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_stack_is_no_single_weight():
+    q = torch.zeros(2, 256, 256, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    w = q8.QWeightBlock(q, torch.zeros(2, 2, 2))
+    with pytest.raises(ValueError, match="stack of experts"):
+        q8._one_weight(w)
