@@ -742,8 +742,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                 }
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+            if (lane == 0) mbar_arrive_relaxed(&tempty_bar[buf]);
         }
         // Quad g of the tile goes to rank g % splits, slot [rank][team][g / splits][channel].
         const uint32_t dst = smem_addr(red) + ((rank * C::TEAMS + team) * qpo * kBM + ch) * 16u;

@@ -562,8 +562,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                     }
                 }
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                if (lane == 0) mbar_arrive_relaxed(&tempty_bar[buf]);
             }
             // From here on the sums are in local memory, so that loops over the
             // tokens need not be unrolled: unrolled, this part is tens of KB of
@@ -967,8 +966,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                         }
                     }
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+                    if (lane == 0) mbar_arrive_relaxed(&tempty_bar[buf]);
                     buf ^= 1;
                     if (buf == 0) bphase ^= 1;
                 }
