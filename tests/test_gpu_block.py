@@ -223,3 +223,40 @@ def test_empty_calls():
     assert q8.q8_linear_fp8_block_dynamic(X, w).shape == (0, 64)
     a = q8.q8_quantize_act_block(X)
     assert q8.q8_linear_fp8_block(a, w).shape == (0, 64)
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (5, 19200, 96), (16, 19216, 160),        # more 128-channel tiles than SMs, quantized inside
+    (24, 8192, 288), (48, 19200, 64),        # the two-team decode GEMM, split and not
+    (96, 4608, 96), (250, 4112, 160),        # tiles with fewer than 257 tokens
+    (130, 2048, 1056), (70, 4096, 32)])      # 128-token decode GEMM; one K group
+def test_linear_where_the_kernels_change(m, n, k):
+    X, w, b, a, y, mag = _linear_case(m, n, k, torch.bfloat16, bias=True, seed=5)
+    Y = q8.q8_linear_fp8_block(a, w, b)
+    R.check(Y, y, mag, k, f"linear {m}x{n}x{k}")
+    D = q8.q8_linear_fp8_block_dynamic(X, w, b)
+    assert torch.equal(D.view(torch.int16), Y.view(torch.int16))
+
+
+def test_calls_that_overlap_on_two_streams():
+    cases = [_linear_case(m, n, 1056, torch.bfloat16, True, seed=m) for m, n in ((3, 528), (60, 528), (300, 784), (100, 4608))]
+    want = [q8.q8_linear_fp8_block_dynamic(X, w, b) for X, w, b, *_ in cases]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for r in range(10):
+        for i, s in enumerate(streams):
+            c = (r + 2 * i) % len(cases)
+            outs.append((c, q8.q8_linear_fp8_block_dynamic(*cases[c][:3], stream=s)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.view(torch.int16), want[c].view(torch.int16)) for c, o in outs)
+    assert q8.q8_get_device_status() == 0
+
+
+def test_stack_of_one_and_wrong_stack():
+    X, w, b, a, y, mag = _linear_case(40, 272, 288, torch.bfloat16, False)
+    one = q8.QWeightBlock(w.codes[None], w.scale[None])
+    R.check(q8.q8_linear_fp8_block(a, one), y, mag, 288, "stack of one")
+    two = q8.q8_quantize_weight_block(_weight(272, 288, 1, 2).to(DEV))
+    for call in (lambda: q8.q8_linear_fp8_block(a, two), lambda: q8.q8_linear_fp8_block_dynamic(X, two)):
+        with pytest.raises(ValueError):
+            call()

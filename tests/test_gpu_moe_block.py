@@ -265,3 +265,15 @@ def test_weights_requantized_in_place_before_the_layer():
             assert q8.lib().q8_quantize_weight_block(W.data_ptr(), q8.Q8_BF16, E, n, kk, kk, d.codes.data_ptr(), d.scale.data_ptr(), s) == 0
         Y = q8.q8_moe_fp8_block(X, ids, w, w13, w2)
         assert torch.equal(Y.view(torch.int16), want[i].view(torch.int16))
+
+
+@pytest.mark.parametrize("m,E,k,hidden,inter", [(16, 64, 8, 1024, 640), (64, 24, 6, 1568, 384), (30, 12, 4, 2048, 512)])
+def test_layer_with_tiles_shared_by_several_ctas(m, E, k, hidden, inter):
+    # several tiles per CTA, most of them whole, the first and the last shared
+    X = workloads.random_matrix(m, hidden, torch.bfloat16, m)
+    w13, w2 = _weights(E, inter, hidden, 31)
+    ids, w = _choice(m, E, k, 8)
+    Y = q8.q8_moe_fp8_block(X.to(DEV), ids, w, w13, w2)
+    _check(Y, X, ids, w, w13, w2)
+    for _ in range(5):
+        assert torch.equal(q8.q8_moe_fp8_block(X.to(DEV), ids, w, w13, w2).view(torch.int16), Y.view(torch.int16))
