@@ -1017,12 +1017,14 @@ q8_status launch_block_linear(const BlockLinearArgs& a, cudaStream_t s) {
     }
     if (a.m <= 16) return run_block_decode<16, false, __half>(a, s);
     if (a.m <= 32) return run_block_decode<32, false, __half>(a, s);
-    if (a.m <= 64) return run_block_decode<64, false, __half>(a, s);
-    // Up to 256 tokens as long as K can be split at least four ways in one wave;
-    // with more output the tile kernel's larger tiles are faster (256x4096x4096:
-    // 15.3 us split, 12.9 in tiles; 128x4096x4096: 10.1 and 12.3; 200x14336x4096:
-    // 49 and 25).
-    if (a.m <= 2 * kBM && (a.m + kBM - 1) / kBM * ((a.n + kBM - 1) / kBM) <= 32)
+    // From 33 tokens on the decode GEMM serves where K can be split in one wave
+    // (twice up to 64 tokens, four times up to 256); with more output the tile
+    // kernel's larger tiles are faster (64x8192x4096: 11.4 us split, 12.6 in tiles;
+    // 48x14336x4096: 16.1 and 14.5; 128x4096x4096: 10.1 and 12.3; 256x4096x4096:
+    // 15.3 and 12.9; 200x14336x4096: 49 and 21).
+    const int64_t tiles_n = (a.n + kBM - 1) / kBM;
+    if (a.m <= 64 && tiles_n <= 64) return run_block_decode<64, false, __half>(a, s);
+    if (a.m > 64 && a.m <= 2 * kBM && (a.m + kBM - 1) / kBM * tiles_n <= 32)
         return run_block_decode<128, false, __half>(a, s);
     return run_tiles<false>(a, (a.m + kBM - 1) / kBM, s);
 }
