@@ -517,7 +517,8 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
 // With QX the activation arrives unquantized and eight more warps quantize it
 // on its way into the stages (the codes are those of the activation
 // quantizer): a warp takes four tokens of one K group, and the groups go
-// round the warps, since one such piece is a chain of about 1000 cycles too.
+// round the warps, since one such piece is a chain of about 1000 cycles too
+// (all of a stage's tokens on one warp: 16x14336x4096 16.3 -> 19.6 us).
 //   warp 0 TMA, warp 1 MMA, then the promotion warps, then the quantizing ones.
 
 constexpr int kQxWarps = 8;
@@ -539,7 +540,7 @@ struct BlockDecodeCfg {
     static constexpr int SX_RING = MAX_STAGES + 4;
     static constexpr int STATIC = 4 * 1024 + (QX ? 0 : PROMO * kScaleRing * CW * 4);   // static shared memory, at most
     static constexpr int TMEM_COLS = 2 * TEAMS * NT;   // at least the 32 an allocation takes
-    static_assert(!QX || NT == 16, "the quantizing warps cover 16 tokens");
+    static_assert(!QX || (NT == 16 && TEAMS == 1), "the quantizing warps cover 16 tokens and count on one team to free stages");
 };
 
 template <int NT, bool QX, typename T>
@@ -760,11 +761,16 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         }
         __syncwarp();
     } else if constexpr (QX) {
-        // Piece (group i, quad): 8 lanes per token, 16 values each.
+        // Piece (group i, quad): 8 lanes per token, 16 values each.  A barrier's
+        // parity only tells neighbouring phases apart, so no more warps work than
+        // leave a warp's groups at most nstages apart: its last group then showed
+        // that groups up to i - 2 * nstages have been read (one thread frees the
+        // stages, in their order), and only the use before this one is waited for.
         pdl_wait();
         const int qw = warp - 2 - C::PROMO;
         const int sub = lane & 7, tl = lane / 8;
         const int pieces = my_kb * quads;
+        const int warps = min(kQxWarps, nstages * quads);
         auto load = [&](int piece, Eight<T>& lo, Eight<T>& hi) {
             const int t = piece % quads * 4 + tl;
             const int col = (kb0 + piece / quads) * kBlock + sub * 16;
@@ -777,15 +783,16 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             }
         };
         Eight<T> lo, hi;
-        if (qw < pieces) load(qw, lo, hi);
-        for (int piece = qw; piece < pieces; piece += kQxWarps) {
+        const int first = qw < warps ? qw : pieces;   // the others have nothing to do
+        if (first < pieces) load(first, lo, hi);
+        for (int piece = first; piece < pieces; piece += warps) {
             const int i = piece / quads, t = piece % quads * 4 + tl;
             float s;
             const uint4 w = quantize16<T>(lo, hi, s);
-            if (piece + kQxWarps < pieces) load(piece + kQxWarps, lo, hi);
+            if (piece + warps < pieces) load(piece + warps, lo, hi);
             const int stage = i % nstages, use = i / nstages;
-            if (use > 0 && !mbar_wait_short(&empty_bar[stage], (use - 1) & 1, &abort_sh, p.status)) break;
-            __syncwarp();
+            const bool ok = use == 0 || mbar_wait_short(&empty_bar[stage], (use - 1) & 1, &abort_sh, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
             st_shared_v4(smem + stage * C::STAGE + C::A_BYTES + t * kBKB + ((sub ^ (t & 7)) << 4), w.x, w.y, w.z, w.w);
             if (sub == 0) sx_ring[i % C::SX_RING][t] = s;
             fence_proxy_async_smem();

@@ -260,3 +260,20 @@ def test_stack_of_one_and_wrong_stack():
     for call in (lambda: q8.q8_linear_fp8_block(a, two), lambda: q8.q8_linear_fp8_block_dynamic(X, two)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("m", [1, 2, 4, 5, 9, 16])
+@pytest.mark.parametrize("n,k", [(19200, 4096), (14336, 4128), (4096, 14336), (128, 28672)])
+def test_few_tokens_over_many_groups(m, n, k):
+    # many more K groups per CTA than stages, and with few tokens fewer pieces of a group
+    # than quantizing warps: each warp then skips several uses of a stage
+    X = _spiky(m, k, torch.bfloat16, m).to(DEV)
+    w = q8.q8_quantize_weight_block(_weight(n, k, 3).to(DEV))
+    a = q8.q8_quantize_act_block(X)
+    want = q8.q8_linear_fp8_block(a, w)
+    cols = torch.arange(0, n, max(1, n // 96))
+    y, mag = R.linear(R.act_value(a.codes, a.scale), R.weight_value(w.codes, w.scale)[cols])
+    R.check(want[:, cols.to(DEV)], y, mag, k, f"{m}x{n}x{k}")
+    for _ in range(4):
+        assert torch.equal(q8.q8_linear_fp8_block_dynamic(X, w).view(torch.int16), want.view(torch.int16))
+    assert q8.q8_get_device_status() == 0
