@@ -600,6 +600,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
+    cluster_started();
     pdl_launch_dependents();
 
     if (warp == 0) {
@@ -644,6 +645,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
                     if (issued & (1u << s)) mbar_wait(&full_bar[s], (last_par >> s) & 1, nullptr, nullptr);
         }
         __syncwarp();
+        cluster_wait_started();
     } else if (warp == 1) {
         {
             const bool leader = elect_one();   // one lane issues, as in the pair kernel
@@ -680,6 +682,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             }
         }
         __syncwarp();
+        cluster_wait_started();
     } else if (warp < 2 + C::PROMO) {
         const int q = warp & 3, set = (warp - 2) / 4;
         const int team = C::TEAMS == 2 ? set : 0;
@@ -745,6 +748,9 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             tc_fence_before();
             if (lane == 0) mbar_arrive_relaxed(&tempty_bar[buf]);
         }
+        // The other CTAs have long started: nothing is waited for here as a rule.
+        __syncwarp();
+        cluster_wait_started();
         // Quad g of the tile goes to rank g % splits, slot [rank][team][g / splits][channel].
         const uint32_t dst = smem_addr(red) + ((rank * C::TEAMS + team) * qpo * kBM + ch) * 16u;
         uint32_t owner = static_cast<uint32_t>(c0 / 4 % splits), off = static_cast<uint32_t>(c0 / 4 / splits) * (kBM * 16u);
@@ -803,6 +809,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             }
         }
         __syncwarp();
+        cluster_wait_started();
     }
 
     // Every rank's pushed sums are visible after this barrier; after it no CTA

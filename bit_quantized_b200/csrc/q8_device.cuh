@@ -412,6 +412,20 @@ __device__ __forceinline__ void cluster_sync() {
                      : "memory");
 }
 
+// The same barrier in two halves, for the start of a kernel: a CTA's shared
+// memory may be written by another CTA of its cluster only once that CTA runs,
+// which its residency does not say.  Every thread arrives at the start and waits
+// before its warp's first access to another CTA (or at the end of its role), so
+// that the round trip lies under the work in between.  Relaxed: the arrival says
+// that the CTA runs and publishes nothing.
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait_started() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Programmatic dependent launch: the next kernel in the stream may start its
 // prologue once every CTA of this grid has executed launch_dependents; it
 // calls wait before touching anything this grid writes.

@@ -1,0 +1,32 @@
+"""Block-scaled FP8 on the GPU where its kernels' orders and ranges end."""
+import pytest
+import torch
+
+import workloads
+from tests import block_reference as R
+
+pytestmark = pytest.mark.gpu
+
+from bit_quantized_b200 import q8  # noqa: E402
+
+DEV = "cuda:0"
+
+
+def _operands(m, n, k, seed, dtype=torch.bfloat16):
+    X = workloads.random_matrix(m, k, torch.float32, seed)
+    X.view(-1)[::97] *= 50.0
+    W = workloads.random_matrix(n, k, torch.bfloat16, seed + 1, std=0.02)
+    return X.to(dtype).to(DEV), q8.q8_quantize_weight_block(W.to(DEV))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 128, 1024), (16, 272, 1024), (16, 16, 512), (20, 400, 1024), (50, 128, 896), (100, 256, 256)])
+def test_one_group_per_cta_of_a_cluster(m, n, k):
+    # a CTA pushes its sums to the others after a single K group, launch upon launch
+    X, w = _operands(m, n, k, m + n)
+    a = q8.q8_quantize_act_block(X)
+    y, mag = R.linear(R.act_value(a.codes, a.scale), R.weight_value(w.codes, w.scale))
+    want = q8.q8_linear_fp8_block(a, w)
+    R.check(want, y, mag, k, f"{m}x{n}x{k}")
+    outs = [f(*args) for _ in range(25) for f, args in ((q8.q8_linear_fp8_block, (a, w)), (q8.q8_linear_fp8_block_dynamic, (X, w)))]
+    assert all(torch.equal(o.view(torch.int16), want.view(torch.int16)) for o in outs)
+    assert q8.q8_get_device_status() == 0
