@@ -950,6 +950,7 @@ gemm_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
+    cluster_started();
     // The next kernel (typically the next layer's activation quantizer, which
     // waits for this grid before touching memory) may launch now.
     pdl_launch_dependents();
@@ -995,6 +996,7 @@ gemm_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
                     if (issued & (1u << s)) mbar_wait(&full_bar[s], (last_par >> s) & 1, nullptr, nullptr);
         }
         __syncwarp();
+        cluster_wait_started();
     } else if (warp == 1) {
         if (elect_one()) {
             // A = weights (u8 or s8 for INT8, E4M3), B = tokens.
@@ -1029,6 +1031,7 @@ gemm_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             if (!ok) mbar_wait(&drain_bar, 0, nullptr, nullptr);
         }
         __syncwarp();
+        cluster_wait_started();
     } else {
         // Epilogue warps: push this rank's TMEM partial for token t into the
         // shared memory of the rank that finishes t (t % splits), at slot
@@ -1056,6 +1059,7 @@ gemm_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         bool have = my_kb > 0 && mbar_wait(&tfull_bar, 0, &abort_sh, p.status);
         if (have) tc_fence_after();
         __syncwarp();
+        cluster_wait_started();
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t red_base = smem_addr(red);
 #pragma unroll

@@ -11,7 +11,7 @@ import pytest
 from tests import kernel_source as S
 
 REMOTE = re.compile(r"\b(st_shared_cluster_\w+|mbar_arrive_cluster)\s*\(")
-WRITERS = ["gemm_block_decode_kernel", "gemm_pair_kernel"]
+WRITERS = ["gemm_block_decode_kernel", "gemm_decode_kernel", "gemm_pair_kernel"]
 
 
 @pytest.mark.parametrize("name", WRITERS)
