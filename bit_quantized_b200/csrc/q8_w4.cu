@@ -323,6 +323,8 @@ w4a16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
+    const bool in_cluster = C::SPLIT && splits > 1;
+    if (in_cluster) cluster_started();
     pdl_launch_dependents();
 
     if (warp == 0) {
@@ -376,6 +378,7 @@ w4a16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     }
         }
         __syncwarp();
+        if (in_cluster) cluster_wait_started();
     } else if (warp == 1) {
         if (elect_one()) {
             const uint32_t idesc = make_idesc(1, BF16 ? 1 : 0, BF16 ? 1 : 0, kBM, NT);
@@ -409,6 +412,7 @@ w4a16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             if (!ok) mbar_wait(&drain_bar, 0, nullptr, nullptr);
         }
         __syncwarp();
+        if (in_cluster) cluster_wait_started();
     } else {
         // ---------------- dequantize
         // Two threads per weight row, each expanding one half of the row's
@@ -464,6 +468,7 @@ w4a16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         const bool have = my_kb > 0 && mbar_wait(&tfull_bar, 0, &abort_sh, p.status);
         if (have) tc_fence_after();
         __syncwarp();
+        if (in_cluster) cluster_wait_started();
         const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         if (splits == 1) {
             for (int c = 16 * eh; c < NT && m0 + c < p.m; c += 32) {

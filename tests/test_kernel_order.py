@@ -11,7 +11,11 @@ import pytest
 from tests import kernel_source as S
 
 REMOTE = re.compile(r"\b(st_shared_cluster_\w+|mbar_arrive_cluster)\s*\(")
-WRITERS = ["gemm_block_decode_kernel", "gemm_decode_kernel", "gemm_pair_kernel"]
+WRITERS = ["gemm_block_decode_kernel", "gemm_decode_kernel", "gemm_pair_kernel", "w4a16_kernel"]
+
+
+def test_every_kernel_that_writes_remotely_is_listed():
+    assert sorted(k for k, body in S.kernels().items() if REMOTE.search(body)) == sorted(WRITERS)
 
 
 @pytest.mark.parametrize("name", WRITERS)
