@@ -324,8 +324,8 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
         for (int tile = first_tile; tile < num_tiles && ok; tile += step) {
             for (int kb = 0; kb < num_kb; ++kb) {
                 if (turn == w) {
-                    if (!mbar_wait_short(&tempty_bar[w], bphase ^ 1, &abort_sh, p.status) ||
-                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_short(&tempty_bar[w], bphase ^ 1, &abort_sh, p.status) &&
+                                                 mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status))) {
                         ok = false;
                         break;
                     }
@@ -406,7 +406,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                 for (int j = 0; j < 4; ++j) {
                     const int kb = kb0 + j;
                     if (kb >= num_kb) break;
-                    if (!mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status))) {
                         ok = false;
                         break;
                     }
@@ -655,8 +655,8 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             bool ok = true;
             for (int i = 0; i < my_kb; ++i) {
                 const int n = i / C::TEAMS, buf = i % C::TEAMS * 2 + (n & 1);
-                if (!mbar_wait_short(&tempty_bar[buf], ((n >> 1) & 1) ^ 1, &abort_sh, p.status) ||
-                    !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
+                if (!__all_sync(0xffffffffu, mbar_wait_short(&tempty_bar[buf], ((n >> 1) & 1) ^ 1, &abort_sh, p.status) &&
+                                             mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status))) {
                     ok = false;
                     break;
                 }
@@ -723,14 +723,14 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
             __syncwarp();
             const float swk = sw_ring[warp - 2][slot];
             if constexpr (QX) {
-                if (!mbar_wait_short(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status)) break;
+                if (!__all_sync(0xffffffffu, mbar_wait_short(&sx_bar[i % C::SX_RING], (i / C::SX_RING) & 1, &abort_sh, p.status))) break;
                 if (lane < C::CW) cs[lane] = lane < cn ? sx_ring[i % C::SX_RING][lane] * swk : 0.f;
             } else {
 #pragma unroll
                 for (int c = 0; c < C::CW; c += 32)
                     if (c + lane < C::CW) cs[c + lane] = c + lane < cn ? sxa_ring[warp - 2][slot][c + lane] * swk : 0.f;
             }
-            if (!mbar_wait_short(&tfull_bar[buf], (n >> 1) & 1, &abort_sh, p.status)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait_short(&tfull_bar[buf], (n >> 1) & 1, &abort_sh, p.status))) break;
             __syncwarp();
             if (warp - 2 == team * 4 && lane == 0) mbar_arrive(&empty_bar[i % nstages]);   // the MMAs have read the stage
             tc_fence_after();

@@ -74,7 +74,11 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 // Waits until the barrier phase with the given parity has completed.  Returns
 // false, after recording a timeout, when it does not within `limit_ns` or when
-// another role of the CTA has already aborted (`abort_flag` non-zero).
+// another role of the CTA has already aborted (`abort_flag` non-zero).  Lanes of
+// a warp may get different answers when the limit runs out between their polls:
+// a role that a whole warp runs asks all of them (__all_sync) before it leaves a
+// loop, so that no lane is missing where the warp acts as one (tcgen05.ld,
+// __syncwarp, barriers).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
                                           volatile int* abort_flag, int* status,
                                           uint64_t limit_ns = kWaitLimitNs) {

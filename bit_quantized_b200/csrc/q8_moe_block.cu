@@ -449,8 +449,8 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 int n = team ? n_odd : n_even;
                 for (int kb = k0; kb < k1; ++kb, ++n) {
                     const int buf = team * 2 + (n & 1);
-                    if (!mbar_wait_short(&tempty_bar[buf], ((n >> 1) & 1) ^ 1, &abort_sh, p.status) ||
-                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_short(&tempty_bar[buf], ((n >> 1) & 1) ^ 1, &abort_sh, p.status) &&
+                                                 mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status))) {
                         ok = false;
                         break;
                     }
@@ -829,8 +829,8 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 const int cnt = list.base[a + 1] - list.base[a];
                 const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((cnt + 15) / 16 * 16));
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) ||
-                        !mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_short(&tempty_bar[buf], bphase ^ 1, &abort_sh, p.status) &&
+                                                 mbar_wait_short(&full_bar[stage], phase, &abort_sh, p.status))) {
                         ok = false;
                         break;
                     }

@@ -31,3 +31,34 @@ def test_remote_shared_memory_after_the_cluster_started(name):
         assert role.count("cluster_wait_started()") == 1
         write = REMOTE.search(role)
         assert write is None or role.index("cluster_wait_started()") < write.start()
+
+
+def _leaves(body):
+    """Loops and roles that a warp leaves after a wait: (wait, text up to the break) outside single-thread blocks."""
+    found, stack, start = [], [], 0
+    for i, c in enumerate(body):
+        if c == "{":
+            stack.append(bool(re.search(r"elect_one\(\)|\bleader\b|\bthreadIdx\.x == 0|lane == 0", body[start:i])))
+        elif c == "}":
+            stack.pop()
+        elif body.startswith("mbar_wait", i) and not any(stack):
+            head = body[start:i + body[i:].index(";")]
+            tail = body[i:]
+            stop = re.search(r"\bbreak;|\n\s*__syncwarp\(\);", tail)
+            if stop and tail[stop.start():].startswith("break"):
+                found.append((head.strip(), head + tail[:stop.end()]))
+        if c in "{};":
+            start = i + 1
+    return found
+
+
+BLOCK_KERNELS = ["gemm_block_tile_kernel", "gemm_block_decode_kernel", "moe_up_kernel", "moe_down_kernel"]
+
+
+@pytest.mark.parametrize("name", BLOCK_KERNELS)
+def test_a_warp_leaves_a_wait_as_one(name):
+    # a limit that runs out between two lanes' polls must not split a warp before tcgen05.ld or __syncwarp
+    leaves = _leaves(S.kernels()[name])
+    assert len(leaves) >= 2
+    for wait, until_break in leaves:
+        assert "__all_sync(" in until_break, wait
