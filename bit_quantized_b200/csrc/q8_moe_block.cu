@@ -548,6 +548,7 @@ moe_up_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ C
                 ++used;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                __syncwarp();                               // every lane's columns of cs (a vote orders no memory)
                 tc_fence_after();
                 const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * 2 * NT;
 #pragma unroll
@@ -954,6 +955,7 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                     ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
+                    __syncwarp();                // every lane's columns of cs (a vote orders no memory)
                     tc_fence_after();
                     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * NT;
 #pragma unroll

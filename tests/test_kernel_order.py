@@ -62,3 +62,15 @@ def test_a_warp_leaves_a_wait_as_one(name):
     assert len(leaves) >= 2
     for wait, until_break in leaves:
         assert "__all_sync(" in until_break, wait
+
+
+@pytest.mark.parametrize("name", ["gemm_block_decode_kernel", "moe_up_kernel", "moe_down_kernel"])
+def test_column_scales_are_ordered_before_their_readers(name):
+    # a lane writes its columns of cs, promote reads all of them in every lane: a vote or a barrier's
+    # poll between them orders no shared memory
+    body = S.kernels()[name]
+    writes = [m.end() for m in re.finditer(r"\bcs\[[^]]*\] = ", body)]
+    assert writes
+    for at in writes:
+        use = re.search(r"\bpromote\(", body[at:])
+        assert "__syncwarp();" in body[at:at + use.start()]
