@@ -575,7 +575,7 @@ gemm_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint32_t bphase = 0;
         for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
             const TileRef tr = tile_ref(tile);
-            if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status))) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * C::BUF_COLS;
             es.row0 = tr.a_row + q * 32;
@@ -851,7 +851,7 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint32_t bphase = 0;
         for (int tile = pair; tile < num_tiles; tile += npairs) {
             const TileRef tr = tile_ref(tile);
-            if (!mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&tfull_bar[buf], bphase, &abort_sh, p.status))) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * C::BUF_COLS;
             es.row0 = tr.a_row + static_cast<int>(rank) * kBM + q * 32;
