@@ -9,9 +9,9 @@
 
 #include <cstdint>
 #include <mutex>
-#include <unordered_map>
 
 #include "q8_device.cuh"
+#include "q8_smem.h"
 
 namespace q8 {
 namespace {
@@ -168,33 +168,6 @@ inline int sm_count() {
     }
     cached[dev] = n;
     return n;
-}
-
-// The dynamic shared-memory limit is a per-kernel, per-device attribute: it is
-// set once (to the largest size asked for) instead of on every launch, which
-// keeps the host side of a call short.
-template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-    static std::mutex mu;
-    static std::unordered_map<const void*, int> done[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-        cudaGetLastError();
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    }
-    const void* key = reinterpret_cast<const void*>(kernel);
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        auto it = done[dev].find(key);
-        if (it != done[dev].end() && it->second >= bytes) return cudaSuccess;
-    }
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) {
-        std::lock_guard<std::mutex> lk(mu);
-        int& v = done[dev][key];
-        if (bytes > v) v = bytes;
-    }
-    return e;
 }
 
 // Pairs that fit on the device at once (clusters of two 1-CTA-per-SM CTAs),

@@ -43,6 +43,7 @@
 
 #include "q8_device.cuh"
 #include "q8_internal.h"
+#include "q8_smem.h"
 
 namespace q8 {
 namespace {
@@ -623,10 +624,7 @@ q8_status run_w4(const W4Args& a, cudaStream_t s) {
     const int smem = astages * kABytes + qstages * C::QSLOT + C::RED_BYTES + 1024;
 
     auto kern = w4a16_kernel<NT, BF16>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return Q8_ERR_LAUNCH;
-    }
+    if (set_smem(kern, smem) != cudaSuccess) return Q8_ERR_LAUNCH;
     W4Params p;
     p.m = static_cast<int>(a.m);
     p.n = static_cast<int>(a.n);

@@ -1,4 +1,6 @@
 """Block-scaled FP8 on the GPU where its kernels' orders and ranges end."""
+import threading
+
 import pytest
 import torch
 
@@ -30,3 +32,25 @@ def test_one_group_per_cta_of_a_cluster(m, n, k):
     outs = [f(*args) for _ in range(25) for f, args in ((q8.q8_linear_fp8_block, (a, w)), (q8.q8_linear_fp8_block_dynamic, (X, w)))]
     assert all(torch.equal(o.view(torch.int16), want.view(torch.int16)) for o in outs)
     assert q8.q8_get_device_status() == 0
+
+
+def test_calls_from_two_host_threads():
+    # one kernel with several ring lengths, and with them shared-memory sizes
+    cases = [_operands(m, n, k, 5) for m, n, k in ((20, 128, 256), (20, 16, 4096), (24, 4096, 512), (30, 272, 8192))]
+    want = [q8.q8_linear_fp8_block_dynamic(X, w) for X, w in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(order, stream):
+        with torch.cuda.stream(stream):
+            for i in order * 20:
+                Y = q8.q8_linear_fp8_block_dynamic(*cases[i])
+                if not torch.equal(Y.view(torch.int16), want[i].view(torch.int16)):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(order, torch.cuda.Stream())) for order in ([0, 1, 2, 3], [3, 2, 1, 0])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and q8.q8_get_device_status() == 0
