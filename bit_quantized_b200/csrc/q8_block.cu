@@ -401,15 +401,16 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     ++sw;
                 }
             }
-            for (int kb0 = 0; kb0 < num_kb && ok; kb0 += 4) {
+            for (int kb0 = 0; kb0 < num_kb; kb0 += 4) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int kb = kb0 + j;
                     if (kb >= num_kb) break;
-                    if (!__all_sync(0xffffffffu, mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status))) {
-                        ok = false;
-                        break;
-                    }
+                    // A wait that ran out ends the tile, not the loop: the warp takes the
+                    // remaining groups without waiting or handing buffers back and votes
+                    // behind them.  A vote in here costs registers that this loop spills
+                    // (4096x8192x8192: 307 us, so 253).
+                    ok = ok && mbar_wait_short(&tfull_bar[buf], bphase, &abort_sh, p.status);
                     __syncwarp();
                     tc_fence_after();
                     const float sc = s_a[j] * s_b[j];
@@ -423,7 +424,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                         if (c + 1 == C::CW / 32) {
                             // All of this warp's part is in registers: the buffer may be written again.
                             tc_fence_before();
-                            if (lane == 0) mbar_arrive_relaxed(&tempty_bar[buf]);
+                            if (lane == 0 && ok) mbar_arrive_relaxed(&tempty_bar[buf]);
                         }
                         promote(acc + c * 16, r, C::TWO && c * 32 >= cut ? sc2 : sc);
                     }
@@ -436,7 +437,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                     if (buf == 0) bphase ^= 1;
                 }
             }
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, ok)) break;
             // A tensor store clips at the output's last row only: chunks that
             // cross an expert's end are stored row by row.
             const bool tma = use_tmy && (GROUPED ? row0 + 32 <= tr.row_end : row0 < tr.row_end);

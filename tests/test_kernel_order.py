@@ -56,7 +56,7 @@ LEAVERS = {name: len(_leaves(body)) for name, body in S.kernels().items() if _le
 
 
 def test_the_kernels_that_leave_waits_are_found():
-    assert LEAVERS == {"gemm_block_tile_kernel": 3, "gemm_block_decode_kernel": 5, "moe_up_kernel": 3, "moe_down_kernel": 3,
+    assert LEAVERS == {"gemm_block_tile_kernel": 2, "gemm_block_decode_kernel": 5, "moe_up_kernel": 3, "moe_down_kernel": 3,
                        "gemm_tile_kernel": 1, "gemm_pair_kernel": 1, "w4a16_kernel": 2}
 
 
@@ -77,3 +77,15 @@ def test_column_scales_are_ordered_before_their_readers(name):
     for at in writes:
         use = re.search(r"\bpromote\(", body[at:])
         assert "__syncwarp();" in body[at:at + use.start()]
+
+
+def test_the_tile_kernels_promotion_votes_behind_a_tile():
+    # it stays in the group loop with what each lane knows, hands no buffer back after a failed wait,
+    # and leaves by a vote
+    promotion = S.roles(S.kernels()["gemm_block_tile_kernel"])[-1]
+    wait = promotion.index("ok = ok && mbar_wait_short(")
+    arrive = promotion.index("mbar_arrive_relaxed(&tempty_bar[buf])")
+    leave = promotion.index("if (!__all_sync(0xffffffffu, ok)) break;")
+    assert wait < arrive < leave < promotion.index("tma_store_2d")
+    assert "if (lane == 0 && ok)" in promotion[wait:arrive] and "break;" not in promotion[wait:leave]
+    assert promotion.count("mbar_wait") == 1
