@@ -191,6 +191,11 @@ struct BlockTileCfg {
     static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
     static constexpr int TMEM_COLS = BN <= 128 ? 256 : 512;
     static constexpr int CW = BN / 2;                      // columns per promotion warp
+    // Groups that the scales are fetched ahead of their use: a group of narrow
+    // tiles is short, and wide ones leave few registers (512x4096x4096: 14.5 us
+    // with four groups ahead, 14.0 with eight; 4096x8192x8192: 299 us with four,
+    // which spill inside the group loop, 245 with two).
+    static constexpr int AHEAD = BN == 128 ? 8 : BN == 192 ? 4 : 2;
     // 96 columns may reach into a second weight block (at a multiple of 32).
     static constexpr bool TWO = CW % 128 != 0 && 128 % CW != 0;
     static constexpr int SMEM = STAGES * STAGE + STORE + 1024;
@@ -383,27 +388,27 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
             float2 acc[C::CW / 2];
 #pragma unroll
             for (int i = 0; i < C::CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            // Scales are fetched four groups ahead of their use.  The loads are
+            // Scales are fetched AHEAD groups before their use.  The loads are
             // volatile and the products are formed at the use: left to itself,
-            // the compiler forms them right behind the loads, and every fourth
-            // group then waits about 2000 cycles for memory.
-            float s_a[4], s_b[4], s_c[C::TWO ? 4 : 1];
+            // the compiler forms them right behind the loads, and every group
+            // then waits for memory.
+            float s_a[C::AHEAD], s_b[C::AHEAD], s_c[C::TWO ? C::AHEAD : 1];
             auto fetch = [&](int j) {
-                s_a[j] = ld_scale(sx);
-                s_b[j] = ld_scale(sw);
-                if constexpr (C::TWO) s_c[j] = ld_scale(sw + to_next);
+                s_a[j] = ld_act_scale(sx);
+                s_b[j] = ld_weight_scale(sw);
+                if constexpr (C::TWO) s_c[j] = ld_weight_scale(sw + to_next);
             };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < C::AHEAD; ++j) {
                 fetch(j);
                 if (j + 1 < num_kb) {              // past the end: loaded again, not used
                     sx += p.m;
                     ++sw;
                 }
             }
-            for (int kb0 = 0; kb0 < num_kb; kb0 += 4) {
+            for (int kb0 = 0; kb0 < num_kb; kb0 += C::AHEAD) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < C::AHEAD; ++j) {
                     const int kb = kb0 + j;
                     if (kb >= num_kb) break;
                     // A wait that ran out ends the tile, not the loop: the warp takes the
@@ -429,7 +434,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
                         promote(acc + c * 16, r, C::TWO && c * 32 >= cut ? sc2 : sc);
                     }
                     fetch(j);
-                    if (kb + 5 < num_kb) {
+                    if (kb + C::AHEAD + 1 < num_kb) {
                         sx += p.m;
                         ++sw;
                     }
@@ -457,7 +462,7 @@ gemm_block_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_con
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (4 * i >= nv) break;
-                        const float4 b = __ldg(b4 + i);
+                        const float4 b = b4[i];
                         out[4 * i] = __fadd_rn(out[4 * i], b.x);
                         out[4 * i + 1] = __fadd_rn(out[4 * i + 1], b.y);
                         out[4 * i + 2] = __fadd_rn(out[4 * i + 2], b.z);

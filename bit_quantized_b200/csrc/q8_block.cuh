@@ -110,13 +110,18 @@ struct Eight<float> {
     }
 };
 
-// A scale of the tile kernel's promotion.  Volatile keeps it where it stands.
-// Non-coherent, because an ordinary load would be waited for by every barrier
-// operation that follows (4096x8192x8192: 295 us, with asynchronous copies 265,
-// so 248): it is issued after the programmatic-launch wait, no earlier read of
-// this kernel can have cached the line, and nothing writes the scales from then
-// on.
-__device__ __forceinline__ float ld_scale(const float* p) {
+// Scales of the tile kernel's promotion.  Volatile keeps the loads where they
+// stand.  An activation's may be written by the previous kernel while this one
+// is resident, so they are read by ordinary loads behind the programmatic-launch
+// wait.  A weight's are complete before this kernel starts (the launch-overlap
+// rule of the interface) and stay as they are: read-only data.
+__device__ __forceinline__ float ld_act_scale(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float ld_weight_scale(const float* p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;

@@ -4,6 +4,7 @@ A CTA may write another CTA's shared memory once that CTA has started
 (programming guide, distributed shared memory), and a cluster barrier is the
 only thing that says so.
 """
+import os
 import re
 
 import pytest
@@ -89,3 +90,17 @@ def test_the_tile_kernels_promotion_votes_behind_a_tile():
     assert wait < arrive < leave < promotion.index("tma_store_2d")
     assert "if (lane == 0 && ok)" in promotion[wait:arrive] and "break;" not in promotion[wait:leave]
     assert promotion.count("mbar_wait") == 1
+
+
+def test_only_weight_scales_are_read_as_constant_data():
+    # with programmatic launch an earlier kernel may write activations, their scales, biases and outputs
+    # while a kernel is resident, so only the weights' side may go through the read-only path
+    files = [f for f in sorted(os.listdir(S.CSRC)) if re.search(r"block|tile|device", f)]
+    assert len(files) == 5
+    for f in files:
+        s = S.text(f)
+        assert "__ldg" not in s
+        for m in re.finditer(r"\.nc\b", s):
+            assert re.findall(r"float (\w+)\(", s[:m.start()])[-1] == "ld_weight_scale"
+        for arg in re.findall(r"[^t] ld_weight_scale\(([^;]*)\);", s):
+            assert arg.startswith("sw")
