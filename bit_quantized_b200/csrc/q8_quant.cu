@@ -47,11 +47,13 @@ template <> struct VecOf<__half> { static constexpr int N = 8; };
 template <> struct VecOf<__nv_bfloat16> { static constexpr int N = 8; };
 template <> struct VecOf<float> { static constexpr int N = 4; };
 
-// Read-only streaming load (not volatile, so the compiler can issue all of a
-// thread's loads before the first use and keep them in flight together).
+// Streaming load of an input.  With programmatic launch the previous kernel may
+// still write it while this one is resident, so it is no read-only (.nc) load,
+// and it is volatile: nothing moves it before the wait for that kernel.  A
+// thread's loads stand together in the code and stay in flight together.
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
     uint4 u;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
         : "l"(p));
     return u;
