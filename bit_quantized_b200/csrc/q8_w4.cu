@@ -428,12 +428,15 @@ w4a16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         int qs = 0, as = 0;
         uint32_t qph = 0, aph = 0;
         for (int i = 0; i < my_kb; ++i) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&q_full[qs], qph, &abort_sh, p.status))) break;
+            bool ready = mbar_wait(&q_full[qs], qph, &abort_sh, p.status);
             const uint8_t* qsl = q_ring + qs * C::QSLOT + C::X_BYTES;
             const uint4 cw = *reinterpret_cast<const uint4*>(qsl + row * 32 + half * 16);
             const float* ssl = reinterpret_cast<const float*>(qsl + kQBytes);
             const uint32_t sc = __float_as_uint(ssl[(gps == 2 ? half * kBM : 0) + row]);
-            if (!__all_sync(0xffffffffu, mbar_wait(&a_empty[as], aph ^ 1, &abort_sh, p.status))) break;
+            ready = ready && mbar_wait(&a_empty[as], aph ^ 1, &abort_sh, p.status);
+            // One vote for both waits (512x4096x4096: 37.2 us, 38.2 with one each,
+            // 38.6 with one at the barrier below).
+            if (!__all_sync(0xffffffffu, ready)) break;
             const uint32_t dst = a_row + as * kABytes;
             const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
             const uint64_t s2 = pair(sc, sc);
