@@ -615,7 +615,7 @@ def _bytes(workspace: Optional[torch.Tensor]) -> int:
 def _ld(t: torch.Tensor) -> int:
     # The stride of a single row means nothing to torch: the row's length stands for it.
     rows, cols = t.shape
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    return t.stride(0) if rows > 1 else cols
 
 
 def _one_weight(w: QWeightBlock):

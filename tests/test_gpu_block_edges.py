@@ -54,3 +54,15 @@ def test_calls_from_two_host_threads():
     for t in threads:
         t.join()
     assert not bad and q8.q8_get_device_status() == 0
+
+
+def test_one_token_with_an_odd_row_stride():
+    X, w = _operands(1, 272, 288, 3)
+    want = q8.q8_linear_fp8_block_dynamic(X, w)
+    odd = torch.as_strided(torch.cat([X[0], X[0, :5]]), (1, 288), (289, 1))
+    out = torch.as_strided(torch.zeros(300, dtype=torch.bfloat16, device=DEV), (1, 272), (277, 1))
+    a = q8.q8_quantize_act_block(odd)
+    ids, p = q8.q8_moe_route(torch.as_strided(X[0], (1, 16), (17, 1)), 2)
+    assert ids.tolist() == [torch.sort(X[0, :16].float(), descending=True, stable=True).indices[:2].tolist()]
+    for Y in (q8.q8_linear_fp8_block_dynamic(odd, w, out=out), q8.q8_linear_fp8_block(a, w)):
+        assert torch.equal(Y.view(torch.int16), want.view(torch.int16))
