@@ -66,3 +66,76 @@ def test_one_token_with_an_odd_row_stride():
     assert ids.tolist() == [torch.sort(X[0, :16].float(), descending=True, stable=True).indices[:2].tolist()]
     for Y in (q8.q8_linear_fp8_block_dynamic(odd, w, out=out), q8.q8_linear_fp8_block(a, w)):
         assert torch.equal(Y.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_quantizers_over_the_whole_range_of_a_type(dtype):
+    # group maxima from the type's largest value, where the low part of 1 / S is subnormal, down to the
+    # scale's floor and below; within a group, values down to the type's smallest
+    big = float(torch.finfo(dtype).max)
+    m, k = 128, 1024
+    g = torch.Generator().manual_seed(11)
+    top = torch.logspace(0, -40, m, base=10.0, dtype=torch.float64)[:, None] * big
+    X = top * torch.exp2(-40.0 * torch.rand(m, k, generator=g, dtype=torch.float64) ** 2)
+    X[:, ::128] = top                                          # every group's absmax
+    X[:, 1::64] = top * (torch.randint(0, 449, (m, 16), generator=g) / 448.0)
+    X = (X * torch.where(torch.rand(m, k, generator=g) < 0.5, -1.0, 1.0)).to(dtype)
+    assert torch.isfinite(X.float()).all()
+    Q, S = R.quant_act(X)
+    a = q8.q8_quantize_act_block(X.to(DEV))
+    assert torch.equal(a.scale.cpu().double(), S)
+    assert torch.equal(a.codes.cpu().float().double(), Q) and torch.equal(torch.signbit(a.codes.cpu().float()), torch.signbit(Q))
+    for W in (X, X.flip(0)[:16], X[:16]):                      # 128 x 128 blocks of both ends of the range
+        Q, S = R.quant_weight(W)
+        w = q8.q8_quantize_weight_block(W.to(DEV).contiguous())
+        assert torch.equal(w.scale.cpu().double(), S)
+        assert torch.equal(w.codes.cpu().float().double(), Q) and torch.equal(torch.signbit(w.codes.cpu().float()), torch.signbit(Q))
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 272, 288), (20, 272, 416), (50, 400, 288), (100, 256, 544), (48, 9216, 96), (300, 784, 416)])
+def test_activation_codes_with_a_row_stride(m, n, k):
+    X, w = _operands(m, n, k, m)
+    a = q8.q8_quantize_act_block(X)
+    y, mag = R.linear(R.act_value(a.codes, a.scale), R.weight_value(w.codes, w.scale))
+    wide = torch.full((m, k + 48), 0x7E, dtype=torch.uint8, device=DEV)     # 448 beside every row
+    wide[:, :k] = a.codes.view(torch.uint8)
+    s = q8.QActBlock(wide.view(R.F8)[:, :k], a.scale)
+    Y = q8.q8_linear_fp8_block(s, w)
+    R.check(Y, y, mag, k, f"strided codes {m}x{n}x{k}")
+    assert torch.equal(Y.view(torch.int16), q8.q8_linear_fp8_block(a, w).view(torch.int16))
+
+
+def test_grouped_activation_codes_with_a_row_stride():
+    counts, n, k = (33, 0, 140, 7), 272, 416
+    m, E = sum(counts), len(counts)
+    X = _operands(m, 16, k, 9)[0]
+    w = q8.q8_quantize_weight_block(workloads.random_matrix(E * n, k, torch.bfloat16, 3, std=0.02).view(E, n, k).to(DEV))
+    a = q8.q8_quantize_act_block(X)
+    wide = torch.full((m, k + 16), 0x7E, dtype=torch.uint8, device=DEV)
+    wide[:, :k] = a.codes.view(torch.uint8)
+    off = torch.tensor([0, 33, 33, 173, 180], dtype=torch.int32, device=DEV)
+    Y = q8.q8_linear_fp8_block_grouped(q8.QActBlock(wide.view(R.F8)[:, :k], a.scale), w, off)
+    x, lo = R.act_value(a.codes, a.scale), 0
+    for e, c in enumerate(counts):
+        y, mag = R.linear(x[lo:lo + c], R.weight_value(w.codes[e], w.scale[e]))
+        R.check(Y[lo:lo + c], y, mag, k, f"expert {e}")
+        lo += c
+
+
+@pytest.mark.parametrize("offsets,spans", [
+    ([-5, 40, 30, 900], [(0, 0, 40), (2, 40, 150)]),           # below 0, falling, past the last row
+    ([10, 60, 60, 149], [(0, 10, 60), (2, 60, 149)]),          # rows before the first expert and after the last
+    ([200, 300, 400, 500], []), ([0, 0, 0, -7], [])])
+def test_grouped_offsets_are_clamped(offsets, spans):
+    n, k, m = 144, 256, 150
+    X = _operands(m, 16, k, 1)[0]
+    w = q8.q8_quantize_weight_block(workloads.random_matrix(3 * n, k, torch.bfloat16, 2, std=0.02).view(3, n, k).to(DEV))
+    a = q8.q8_quantize_act_block(X)
+    Y = torch.full((m, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    q8.q8_linear_fp8_block_grouped(a, w, torch.tensor(offsets, dtype=torch.int32, device=DEV), out=Y)
+    x, stays = R.act_value(a.codes, a.scale), torch.ones(m, dtype=torch.bool)
+    for e, lo, hi in spans:
+        y, mag = R.linear(x[lo:hi], R.weight_value(w.codes[e], w.scale[e]))
+        R.check(Y[lo:hi], y, mag, k, f"expert {e}")
+        stays[lo:hi] = False
+    assert (Y[stays.to(DEV)] == 7.0).all()
