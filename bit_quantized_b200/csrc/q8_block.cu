@@ -654,7 +654,7 @@ gemm_block_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_c
         cluster_wait_started();
     } else if (warp == 1) {
         {
-            const bool leader = elect_one();   // one lane issues, as in the pair kernel
+            const bool leader = elect_one();   // one lane issues, as in the tile kernel
             const uint32_t idesc = make_idesc(1, 0, 0, kBM, static_cast<uint32_t>((mt + 15) / 16 * 16));
             int stage = 0;
             uint32_t phase = 0;

@@ -774,8 +774,11 @@ moe_down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             tma_prefetch_desc(&tmH);
             uint32_t issued = 0, last_par = 0;
             bool ok = true;
-            // Pass 0 asks for the first ring's weights, before the up
-            // projection is done; pass 1 for everything else.
+            // Pass 0 asks for the first ring's weights without waiting for the up
+            // projection, pass 1 for everything else.  An SM holds no CTA of both
+            // projections (registers, shared memory, with 64 tokens TMEM too), so this
+            // one starts when an up CTA has left, and the head start is the time from
+            // there to the end of the last up CTA.
             const int first = min(s_end - s_begin, C::STAGES);
             for (int pass = 0; pass < 2 && ok; ++pass) {
                 if (pass == 1) pdl_wait();
