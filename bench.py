@@ -578,7 +578,7 @@ def load_profile_traffic(kernel_tag: str):
 
 # Sources the GEMM kernels are compiled from (a traffic entry stays valid
 # while these are unchanged).
-GEMM_SOURCES = ("q8_device.cuh", "q8_gemm.cu", "q8_qmath.cuh")
+GEMM_SOURCES = ("q8_device.cuh", "q8_gemm.cu", "q8_qmath.cuh", "q8_tile.cuh")
 
 
 def source_hash() -> str:
